@@ -432,6 +432,126 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
                               int64_t cols, const float *L_root, const float *R_root, const msign_coeffs *coeffs,
                               void *workspace, size_t workspace_bytes, msign_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the layer around the optimizer step (no counterpart on the
+ * pages): the norm in front of a feed-forward block, the gated block itself
+ * and its gradients -- the matrices that muon_step updates and the gradients
+ * it eats -- and the 8-bit product that serves the trained weights.
+ *
+ * They were added without a change to any earlier declaration, so the ABI
+ * version number stays where it was.
+ *
+ * A matrix argument of these entry points is `rows` rows of dense elements,
+ * a row stride (in elements) apart: 0 means back to back, otherwise at least
+ * the row's length (MSIGN_ERR_INVALID_ARG else).  Rows behind the last one
+ * and elements between rows are neither read nor written.  Any alignment and
+ * any size is taken; bases on 16-byte boundaries and strides of whole 16-byte
+ * pieces run fastest (a product whose operands lack that first copies them
+ * into the workspace, which is what its *_workspace_size query counts).
+ * Row counts and widths are at most 2^30 (MSIGN_ERR_UNSUPPORTED beyond).
+ * Two calls that may run at the same time, two captured graphs among them,
+ * need a workspace each.  Results do not depend on the order in which the
+ * GPU runs a call's blocks: the same inputs give the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* rms_norm: s = x + residual, rounded to io_dtype (s = x without a
+ * residual); y = s * weight / sqrt(mean(s^2) + eps) for each row.  The norm is that
+ * of the rounded sum, which is what rms_norm_backward is given.  Squares are
+ * summed and y is formed in fp32.
+ *   residual, sum_out  may be NULL; sum_out needs a residual, and may be x
+ *                      or residual itself (same address and stride)
+ *   weight             cols elements of w_dtype (io_dtype or MSIGN_FP32), or
+ *                      NULL for ones
+ *   y                  may be x or residual itself, where that is not
+ *                      sum_out; no other overlap is allowed
+ *   eps                >= 0 and finite (a row of zeros with eps 0 gives NaN) */
+msign_status rms_norm(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
+                      msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                      int64_t r_stride, int64_t y_stride, int64_t s_stride, float eps, msign_stream_t stream);
+
+/* rms_norm_q8: the same with y quantised to int8, one scale a row: scale =
+ * max|y| / 127 and q = y / scale rounded to the nearest (ties to even), from
+ * the fp32 y.  A row of zeros gives scale 0 and q 0.  A row that holds a NaN
+ * or an infinity gives a scale that is one and q 0: what it stands for, and
+ * every product with it, is NaN. */
+msign_status rms_norm_q8(const void *x, const void *residual, const void *weight, int8_t *q, float *scale,
+                         void *sum_out, msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols,
+                         int64_t x_stride, int64_t r_stride, int64_t q_stride, int64_t s_stride, float eps,
+                         msign_stream_t stream);
+
+/* rms_norm_backward: gradients of rms_norm from dy, the stored sum s (or x)
+ * and, optionally, dsum, the gradient that reaches s past the norm: with
+ * n = s / sqrt(mean(s^2) + eps),
+ *   dx = (dy w - n mean(dy w n)) / sqrt(mean(s^2) + eps) + dsum
+ * (the gradient of x and of residual alike), dw = sum over rows of dy n.
+ * Sums are fp32; dx is io_dtype, dw is w_dtype.
+ *   weight, dsum  may be NULL
+ *   dw            may be NULL (then no workspace is needed)
+ * Outputs must not overlap inputs.  rows = 0 writes dw = 0. */
+size_t rms_norm_backward_workspace_size(int64_t rows, int64_t cols);
+
+msign_status rms_norm_backward(const void *dy, const void *sum, const void *weight, const void *dsum, void *dx,
+                               void *dw, msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols,
+                               int64_t dy_stride, int64_t sum_stride, int64_t dsum_stride, int64_t dx_stride, float eps,
+                               void *workspace, size_t workspace_bytes, msign_stream_t stream);
+
+/* i8_matmul: out[i][j] = (sum over k of a[i][k] b[j][k]) a_scale[i]
+ * b_scale[j], e.g. the output of rms_norm_q8 times a weight matrix (out
+ * features x in features) with a scale for each output channel.  The integer
+ * sum is exact (k < 2^17, MSIGN_ERR_UNSUPPORTED beyond); it is rounded to
+ * fp32, multiplied by the one scale, then the other, and rounded to
+ * out_dtype.  k = 0 writes zeros.
+ *   a, b      m x k and n x k int8 (all of -128..127)
+ *   workspace i8_matmul_workspace_size() bytes (0 for operands on 16-byte
+ *             boundaries with strides of whole 16-byte pieces) */
+size_t i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, const int8_t *a, int64_t a_stride, const int8_t *b,
+                                int64_t b_stride);
+
+msign_status i8_matmul(const int8_t *a, const float *a_scale, const int8_t *b, const float *b_scale, void *out,
+                       msign_dtype out_dtype, int64_t m, int64_t n, int64_t k, int64_t a_stride, int64_t b_stride,
+                       int64_t out_stride, void *workspace, size_t workspace_bytes, msign_stream_t stream);
+
+typedef enum {
+  MSIGN_SILU = 0,
+  MSIGN_GELU = 1,      /* g Phi(g), by the error function */
+  MSIGN_GELU_TANH = 2  /* its tanh form */
+} msign_activation;
+
+/* gated_ffn: gate = x Wg^T, up = x Wu^T, out = act(gate) * up, in one kernel:
+ * both sums are fp32 and only out (and gate and up, where they are asked
+ * for) is rounded.
+ *   x             tokens x d, dtype (MSIGN_BF16 or MSIGN_FP16)
+ *   w_gate, w_up  h x d each with one row stride (the halves of one 2h x d
+ *                 matrix, for instance)
+ *   out           tokens x h
+ *   gate_out,     tokens x h each (row stride pre_stride) for
+ *   up_out        gated_ffn_backward, or both NULL
+ * Outputs must not overlap inputs or each other. */
+size_t gated_ffn_workspace_size(int64_t tokens, int64_t d, int64_t h, const void *x, int64_t x_stride,
+                                const void *w_gate, const void *w_up, int64_t w_stride);
+
+msign_status gated_ffn(const void *x, const void *w_gate, const void *w_up, void *out, void *gate_out, void *up_out,
+                       msign_dtype dtype, msign_activation activation, int64_t tokens, int64_t d, int64_t h,
+                       int64_t x_stride, int64_t w_stride, int64_t out_stride, int64_t pre_stride, void *workspace,
+                       size_t workspace_bytes, msign_stream_t stream);
+
+/* gated_ffn_backward: from dh (tokens x h) and the kept gate and up,
+ *   dg = dh up act'(gate),  du = dh act(gate)   (rounded to dtype)
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+ * dx is dtype; dw_gate and dw_up (h x d, row stride dw_stride) are
+ * grad_dtype: dtype or MSIGN_FP32.  dx may be NULL, and so may dw_gate and
+ * dw_up together.  tokens = 0 writes zero weight gradients.  Outputs must
+ * not overlap inputs or each other. */
+size_t gated_ffn_backward_workspace_size(int64_t tokens, int64_t d, int64_t h, const void *x, int64_t x_stride,
+                                         const void *w_gate, const void *w_up, int64_t w_stride);
+
+msign_status gated_ffn_backward(const void *dh, const void *x, const void *w_gate, const void *w_up, const void *gate,
+                                const void *up, void *dx, void *dw_gate, void *dw_up, msign_dtype dtype,
+                                msign_dtype grad_dtype, msign_activation activation, int64_t tokens, int64_t d,
+                                int64_t h, int64_t dh_stride, int64_t x_stride, int64_t w_stride, int64_t pre_stride,
+                                int64_t dx_stride, int64_t dw_stride, void *workspace, size_t workspace_bytes,
+                                msign_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

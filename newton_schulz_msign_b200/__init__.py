@@ -21,6 +21,9 @@ __all__ = [
     "gram_xxt", "gram_xxt_workspace_size", "gram_ns",
     "gram_ns_workspace_size", "muon_step", "muon_step_workspace_size", "muon_step_route", "mousse_inv_root",
     "mousse_direction",
+    "rms_norm", "rms_norm_q8", "rms_norm_backward", "rms_norm_backward_workspace_size",
+    "i8_matmul", "i8_matmul_workspace_size",
+    "gated_ffn", "gated_ffn_workspace_size", "gated_ffn_backward", "gated_ffn_backward_workspace_size",
     "sync_status", "selftest_timeout", "set_chaining", "library_path",
 ]
 
@@ -424,6 +427,301 @@ def mousse_direction(g, l_root, r_root, out=None, *, coeffs=None, eps=None, impr
     del keep
     check(st, "mousse_direction")
     return out
+
+
+# ---------------------------------------------------------------- layer operators
+
+def _rows_layout(t, name, cols=None):
+    """(rows, cols, stride) of a CUDA tensor whose last dim is dense and whose
+    leading dims step through memory with one row stride (any view of that
+    form, e.g. ``big[:, :n]``); stride 0 means back to back."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dim() < 1:
+        raise ValueError(f"{name} needs at least one dim")
+    width = t.shape[-1]
+    if cols is not None and width != cols:
+        raise ValueError(f"{name} must have {cols} columns, has {width}")
+    rows = math.prod(t.shape[:-1])
+    if rows * width == 0:
+        return rows, width, 0
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: each row (the last dim) must be dense")
+    lead = [(t.shape[d], t.stride(d)) for d in range(t.dim() - 1) if t.shape[d] != 1]
+    if not lead:
+        return rows, width, 0
+    for (sz_o, st_o), (sz_i, st_i) in zip(lead[:-1], lead[1:]):
+        if st_o != st_i * sz_i:
+            raise ValueError(f"{name}: the leading dims must step through memory with one row stride")
+    stride = lead[-1][1]
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap (stride {stride} < {width})")
+    return rows, width, (0 if stride == width else stride)
+
+
+def _like(t, ref, name, shape=None, dtype=None):
+    """The given output, checked, or a new one: like ``ref`` but for shape and dtype."""
+    torch = _torch()
+    shape = tuple(ref.shape) if shape is None else tuple(shape)
+    dtype = ref.dtype if dtype is None else dtype
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    _same_device(t, ref.device, name)
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {shape} of {dtype}")
+    return t
+
+
+def _norm_weight(weight, x):
+    """(dtype code, pointer) of a norm's weight."""
+    torch = _torch()
+    if weight is None:
+        return _dtype_code(x), None
+    _need_cuda(weight, "weight")
+    _same_device(weight, x.device, "weight")
+    if tuple(weight.shape) != (x.shape[-1],):
+        raise ValueError(f"weight must have shape ({x.shape[-1]},)")
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise TypeError("weight must be of the input's dtype or float32")
+    return _dtype_code(weight), weight.data_ptr()
+
+
+def _norm_inputs(x, residual, sum_out):
+    rows, cols, xs = _rows_layout(x, "x")
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+        return rows, cols, xs, 0, None, 0
+    _same_device(residual, x.device, "residual")
+    if residual.shape != x.shape or residual.dtype != x.dtype:
+        raise ValueError("residual must match x in shape and dtype")
+    rs = _rows_layout(residual, "residual")[2]
+    sum_out = _like(sum_out, x, "sum_out")
+    return rows, cols, xs, rs, sum_out, _rows_layout(sum_out, "sum_out")[2]
+
+
+def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_out=None, stream=None):
+    """RMS norm of the last dim of ``x`` (bf16/fp16/fp32), after adding ``residual`` if one is given.
+
+    Returns y = s * weight / sqrt(mean(s^2) + eps), or (y, s) with the sum
+    s = x + residual (rounded to x's dtype) when there is a residual.
+    ``weight``: of x's dtype or float32, None for ones.  ``sum_out`` may be
+    ``x`` or ``residual`` itself, and so may ``out`` where ``sum_out`` is not."""
+    code = _dtype_code(x)
+    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out)
+    wdt, wp = _norm_weight(weight, x)
+    y = _like(out, x, "out")
+    ys = _rows_layout(y, "out")[2]
+    with _torch().cuda.device(x.device):
+        st = _lib.lib().rms_norm(x.data_ptr(), _ptr(residual), wp, y.data_ptr(), _ptr(s), code, wdt, rows, cols, xs, rs,
+                                 ys, ss, float(eps), _stream(stream, x.device))
+    check(st, "rms_norm")
+    return y if residual is None else (y, s)
+
+
+def rms_norm_q8(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, scale_out=None, sum_out=None,
+                stream=None):
+    """``rms_norm`` with y quantised to int8, one float32 scale a row (max|y| / 127): returns
+    (q, scale), or (q, scale, s) when there is a residual.  q * scale[..., None] is what it stands for."""
+    torch = _torch()
+    code = _dtype_code(x)
+    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out)
+    wdt, wp = _norm_weight(weight, x)
+    q = _like(out, x, "out", dtype=torch.int8)
+    qs = _rows_layout(q, "out")[2]
+    scale = _like(scale_out, x, "scale_out", shape=x.shape[:-1], dtype=torch.float32)
+    _need_cuda(scale, "scale_out")
+    with torch.cuda.device(x.device):
+        st = _lib.lib().rms_norm_q8(x.data_ptr(), _ptr(residual), wp, q.data_ptr(), scale.data_ptr(), _ptr(s), code, wdt,
+                                    rows, cols, xs, rs, qs, ss, float(eps), _stream(stream, x.device))
+    check(st, "rms_norm_q8")
+    return (q, scale) if residual is None else (q, scale, s)
+
+
+def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
+    return int(_lib.lib().rms_norm_backward_workspace_size(rows, cols))
+
+
+def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_out=None, dw_out=None, workspace=None,
+                      stream=None):
+    """Gradients of ``rms_norm``: (dx, dw) from ``dy`` and ``s``, the sum that it returned (x without a residual).
+
+    ``dsum``: the gradient that reaches s past the norm, added to dx.  dx is
+    the gradient of x and of the residual alike; dw is None without a weight."""
+    code = _dtype_code(s)
+    rows, cols, zs = _rows_layout(s, "s")
+    strides = []
+    for t, nm in ((dy, "dy"), (dsum, "dsum")):
+        if t is not None:
+            _same_device(t, s.device, nm)
+            if t.shape != s.shape or t.dtype != s.dtype:
+                raise ValueError(f"{nm} must match s in shape and dtype")
+        strides.append(0 if t is None else _rows_layout(t, nm)[2])
+    wdt, wp = _norm_weight(weight, s)
+    dx = _like(dx_out, s, "dx_out")
+    dxs = _rows_layout(dx, "dx_out")[2]
+    dw = None
+    if weight is not None:
+        dw = _like(dw_out, weight, "dw_out")
+        _need_cuda(dw, "dw_out")
+    elif dw_out is not None:
+        raise ValueError("dw_out needs a weight")
+    with _torch().cuda.device(s.device):
+        ws, wsb = _workspace(0 if dw is None else rms_norm_backward_workspace_size(rows, cols), s.device, workspace)
+        st = _lib.lib().rms_norm_backward(dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
+                                          wdt, rows, cols, strides[0], zs, strides[1], dxs, float(eps), _ptr(ws), wsb,
+                                          _stream(stream, s.device))
+    check(st, "rms_norm_backward")
+    return dx, dw
+
+
+def i8_matmul_workspace_size(a, b) -> int:
+    m, k, sa = _rows_layout(a, "a")
+    n, _, sb = _rows_layout(b, "b")
+    return int(_lib.lib().i8_matmul_workspace_size(m, n, k, a.data_ptr(), sa, b.data_ptr(), sb))
+
+
+def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=None, stream=None):
+    """(a b^T) of int8 ``a`` (..., k) and ``b`` (n, k), times float32 ``a_scale`` (...) for each row of a (token)
+    and ``b_scale`` (n,) for each row of b (output channel).
+
+    The integer sums are exact.  ``out_dtype``: bf16 (default), fp16 or
+    float32, or that of ``out``.  ``a`` and ``a_scale`` are what
+    ``rms_norm_q8`` returns."""
+    torch = _torch()
+    for t, nm in ((a, "a"), (b, "b")):
+        if t.dtype != torch.int8:
+            raise TypeError(f"{nm} must be int8")
+    if b.dim() != 2:
+        raise ValueError("b must be (n, k)")
+    m, k, sa = _rows_layout(a, "a")
+    n, _, sb = _rows_layout(b, "b", k)
+    for t, nm, shape in ((a_scale, "a_scale", tuple(a.shape[:-1])), (b_scale, "b_scale", (n,))):
+        _need_cuda(t, nm)
+        _same_device(t, a.device, nm)
+        if t.dtype != torch.float32 or tuple(t.shape) != shape:
+            raise ValueError(f"{nm} must be float32 of shape {shape}")
+    _same_device(b, a.device, "b")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    out = _like(out, a, "out", shape=tuple(a.shape[:-1]) + (n,), dtype=out_dtype)
+    code, so = _dtype_code(out), _rows_layout(out, "out")[2]
+    with torch.cuda.device(a.device):
+        ws, wsb = _workspace(i8_matmul_workspace_size(a, b), a.device, workspace)
+        st = _lib.lib().i8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
+                                  code, m, n, k, sa, sb, so, _ptr(ws), wsb, _stream(stream, a.device))
+    check(st, "i8_matmul")
+    return out
+
+
+_ACTIVATIONS = {"silu": _lib.SILU, "gelu": _lib.GELU, "gelu_tanh": _lib.GELU_TANH}
+
+
+def _activation_code(name) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, not {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _ffn_inputs(x, w_gate, w_up):
+    """(tokens, d, h, x stride, weight stride) of a gated block's inputs."""
+    t, d, xs = _rows_layout(x, "x")
+    if w_gate.dim() != 2 or w_gate.shape != w_up.shape:
+        raise ValueError("w_gate and w_up must be (h, d) of one shape")
+    strides = []
+    for w, nm in ((w_gate, "w_gate"), (w_up, "w_up")):
+        _same_device(w, x.device, nm)
+        if w.dtype != x.dtype:
+            raise TypeError(f"{nm} must be of x's dtype")
+        h, _, st = _rows_layout(w, nm, d)
+        strides.append(st or d)
+    if strides[0] != strides[1]:
+        raise ValueError("w_gate and w_up must have one row stride")
+    return t, d, h, xs, strides[0]
+
+
+def gated_ffn_workspace_size(x, w_gate, w_up) -> int:
+    t, d, h, xs, ws = _ffn_inputs(x, w_gate, w_up)
+    return int(_lib.lib().gated_ffn_workspace_size(t, d, h, x.data_ptr(), xs, w_gate.data_ptr(), w_up.data_ptr(), ws))
+
+
+def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, out=None, gate_out=None, up_out=None,
+              workspace=None, stream=None):
+    """act(x w_gate^T) * (x w_up^T) of ``x`` (..., d) and weights (h, d), bf16 or fp16, in one kernel.
+
+    ``activation``: "silu", "gelu" or "gelu_tanh".  With ``save`` (or
+    ``gate_out`` and ``up_out``) returns (out, gate, up), what
+    ``gated_ffn_backward`` takes; else out."""
+    code, act = _dtype_code(x), _activation_code(activation)
+    t, d, h, xs, ws_ = _ffn_inputs(x, w_gate, w_up)
+    shape = tuple(x.shape[:-1]) + (h,)
+    if (gate_out is None) != (up_out is None):
+        raise ValueError("gate_out and up_out go together")
+    save = save or gate_out is not None
+    out = _like(out, x, "out", shape=shape)
+    gate = _like(gate_out, x, "gate_out", shape=shape) if save else None
+    up = _like(up_out, x, "up_out", shape=shape) if save else None
+    so = _rows_layout(out, "out")[2]
+    sp = _one_stride(gate, "gate_out", up, "up_out", h) if save else 0
+    with _torch().cuda.device(x.device):
+        ws, wsb = _workspace(gated_ffn_workspace_size(x, w_gate, w_up), x.device, workspace)
+        st = _lib.lib().gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), _ptr(gate), _ptr(up),
+                                  code, act, t, d, h, xs, ws_, so, sp, _ptr(ws), wsb, _stream(stream, x.device))
+    check(st, "gated_ffn")
+    return (out, gate, up) if save else out
+
+
+def _one_stride(a, an, b, bn, cols):
+    """The row stride that two matrices share."""
+    sa, sb = (_rows_layout(t, nm)[2] or cols for t, nm in ((a, an), (b, bn)))
+    if sa != sb:
+        raise ValueError(f"{an} and {bn} must have one row stride")
+    return sa
+
+
+def gated_ffn_backward_workspace_size(x, w_gate, w_up) -> int:
+    t, d, h, xs, ws = _ffn_inputs(x, w_gate, w_up)
+    return int(_lib.lib().gated_ffn_backward_workspace_size(t, d, h, x.data_ptr(), xs, w_gate.data_ptr(),
+                                                            w_up.data_ptr(), ws))
+
+
+def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu", grad_dtype=None, need_dx=True,
+                       need_dw=True, dx_out=None, dw_gate_out=None, dw_up_out=None, workspace=None, stream=None):
+    """Gradients of ``gated_ffn``: (dx, dw_gate, dw_up) from ``dh`` and the kept ``gate`` and ``up``.
+
+    ``grad_dtype``: of the weight gradients, x's dtype (default) or float32;
+    either is what ``muon_step`` takes as grads (fp16 blocks: float32).
+    ``need_dx`` / ``need_dw`` False leaves that part out (None in its place)."""
+    torch = _torch()
+    code, act = _dtype_code(x), _activation_code(activation)
+    t, d, h, xs, ws_ = _ffn_inputs(x, w_gate, w_up)
+    if not need_dx and not need_dw:
+        raise ValueError("at least one of need_dx and need_dw")
+    shape = tuple(x.shape[:-1]) + (h,)
+    for g, nm in ((dh, "dh"), (gate, "gate"), (up, "up")):
+        _same_device(g, x.device, nm)
+        if tuple(g.shape) != shape or g.dtype != x.dtype:
+            raise ValueError(f"{nm} must be {shape} of x's dtype")
+    sdh = _rows_layout(dh, "dh")[2]
+    sp = _one_stride(gate, "gate", up, "up", h)
+    if grad_dtype is None:
+        grad_dtype = x.dtype if dw_gate_out is None else dw_gate_out.dtype
+    if grad_dtype not in (x.dtype, torch.float32):
+        raise TypeError("grad_dtype must be x's dtype or float32")
+    dx = _like(dx_out, x, "dx_out") if need_dx else None
+    dwg = _like(dw_gate_out, w_gate, "dw_gate_out", dtype=grad_dtype) if need_dw else None
+    dwu = _like(dw_up_out, w_up, "dw_up_out", dtype=grad_dtype) if need_dw else None
+    sdx = _rows_layout(dx, "dx_out")[2] if need_dx else 0
+    sdw = _one_stride(dwg, "dw_gate_out", dwu, "dw_up_out", d) if need_dw else 0
+    gcode = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}[grad_dtype]
+    with torch.cuda.device(x.device):
+        ws, wsb = _workspace(gated_ffn_backward_workspace_size(x, w_gate, w_up), x.device, workspace)
+        st = _lib.lib().gated_ffn_backward(dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                                           gate.data_ptr(), up.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), code, gcode,
+                                           act, t, d, h, sdh, xs, ws_, sp, sdx, sdw, _ptr(ws), wsb,
+                                           _stream(stream, x.device))
+    check(st, "gated_ffn_backward")
+    return dx, dwg, dwu
 
 
 # ---------------------------------------------------------------- launch records

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(HERE, "libmsign_b200.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(6)
 # msign_dtype
 BF16, FP16, FP32 = 0, 1, 2
+# msign_activation
+SILU, GELU, GELU_TANH = 0, 1, 2
 
 EXPORTS = (
     "msign_abi_version", "msign_status_string", "msign_sync_status",
@@ -27,6 +29,9 @@ EXPORTS = (
     "msign_ns_noalloc_max_bytes", "msign_ns_noalloc",
     "msign_selftest_timeout", "msign_set_chaining", "msign_ns_host_workspace_size", "msign_ns_host",
     "mousse_inv_root_workspace_size", "mousse_inv_root", "mousse_direction_workspace_size", "mousse_direction",
+    "rms_norm", "rms_norm_q8", "rms_norm_backward_workspace_size", "rms_norm_backward",
+    "i8_matmul_workspace_size", "i8_matmul",
+    "gated_ffn_workspace_size", "gated_ffn", "gated_ffn_backward_workspace_size", "gated_ffn_backward",
 )
 
 
@@ -114,6 +119,26 @@ def lib() -> ctypes.CDLL:
         L.mousse_direction_workspace_size.argtypes = [I64, I64, I64]
         L.mousse_direction.restype = I32
         L.mousse_direction.argtypes = [P, P, I32, I64, I64, I64, P, P, ctypes.POINTER(MsignCoeffs), P, SZ, P]
+        L.rms_norm.restype = I32
+        L.rms_norm.argtypes = [P] * 5 + [I32] * 2 + [I64] * 6 + [F32, P]
+        L.rms_norm_q8.restype = I32
+        L.rms_norm_q8.argtypes = [P] * 6 + [I32] * 2 + [I64] * 6 + [F32, P]
+        L.rms_norm_backward_workspace_size.restype = SZ
+        L.rms_norm_backward_workspace_size.argtypes = [I64, I64]
+        L.rms_norm_backward.restype = I32
+        L.rms_norm_backward.argtypes = [P] * 6 + [I32] * 2 + [I64] * 6 + [F32, P, SZ, P]
+        L.i8_matmul_workspace_size.restype = SZ
+        L.i8_matmul_workspace_size.argtypes = [I64, I64, I64, P, I64, P, I64]
+        L.i8_matmul.restype = I32
+        L.i8_matmul.argtypes = [P] * 5 + [I32] + [I64] * 6 + [P, SZ, P]
+        L.gated_ffn_workspace_size.restype = SZ
+        L.gated_ffn_workspace_size.argtypes = [I64, I64, I64, P, I64, P, P, I64]
+        L.gated_ffn.restype = I32
+        L.gated_ffn.argtypes = [P] * 6 + [I32] * 2 + [I64] * 7 + [P, SZ, P]
+        L.gated_ffn_backward_workspace_size.restype = SZ
+        L.gated_ffn_backward_workspace_size.argtypes = [I64, I64, I64, P, I64, P, P, I64]
+        L.gated_ffn_backward.restype = I32
+        L.gated_ffn_backward.argtypes = [P] * 9 + [I32] * 3 + [I64] * 9 + [P, SZ, P]
         _lib = L
     return _lib
 

@@ -17,8 +17,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB_NAME = "libmsign_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = [os.path.join(HERE, "csrc", "msign_b200.cu")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("gemm_sm100.cuh", "elementwise.cuh", "ptx_sm100.cuh")] + [
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("msign_b200.cu", "layer_b200.cu")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("gemm_sm100.cuh", "elementwise.cuh", "ptx_sm100.cuh",
+                                                   "host_sm100.cuh", "norm_sm100.cuh", "dense_sm100.cuh")] + [
     os.path.join(ROOT, "include", "msign_b200.h")]
 
 NVCC_FLAGS = [
@@ -27,6 +28,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC,-O2",
     "-shared",
     "-diag-suppress", "177",
+    "-t", "0",
 ]
 
 

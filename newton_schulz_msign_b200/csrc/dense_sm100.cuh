@@ -1,0 +1,798 @@
+// dense_sm100.cuh - tcgen05 products of a transformer layer: the gated
+// feed-forward block, its gradients, and the int8 product with scales.
+//
+// Two kernels:
+//
+//   dense_pair_kernel    many rows.  Persistent CTA pairs, one 256 x 256
+//                        accumulator tile a pair (tcgen05.mma.cta_group::2),
+//                        two tiles in TMEM so that one is stored while the
+//                        next is formed, a ring of TMA-fed operand stages.
+//   dense_stream_kernel  few rows (a decoding step).  The weights are the
+//                        M operand and stream through once; the tokens are
+//                        the N operand, as narrow as they are.  A cluster of
+//                        CTAs splits K and joins its parts through
+//                        distributed shared memory.
+//
+// A stage holds 128 bytes of K for every operand row whatever the type (64
+// 16-bit elements or 128 int8), so the 16-bit and the int8 forms share the
+// geometry: four MMAs of 32 bytes of K a stage.
+//
+// No load uses cluster multicast: each CTA fetches its own operands.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_sm100.cuh"
+#include "norm_sm100.cuh"
+#include "ptx_sm100.cuh"
+
+namespace msb {
+
+// int8 x int8 -> int32, K = 32 a MMA; pair and single-CTA forms, issued by
+// one elected lane of a converged warp.
+__device__ __forceinline__ void umma_i8_pair_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void umma_i8_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void umma_f16_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void umma_commit_w(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)));
+}
+
+__device__ __forceinline__ void tma_load_3d_w(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)));
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// ---------------------------------------------------------------- activations
+
+enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// g sigmoid(v).  exp(-v) overflows to infinity for very negative v, and the
+// quotient is 0 there, as it should be.
+__device__ __forceinline__ float g_sigmoid(float g, float v) { return __fdividef(g, 1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float act_of(float g, int act) {
+  if (act == ACT_SILU) return g_sigmoid(g, g);
+  if (act == ACT_GELU) return g * normcdff(g);  // (keeps its relative accuracy in the tail, unlike 1 + erf)
+  // (1 + tanh z) / 2 = sigmoid(2 z)
+  return g_sigmoid(g, 2.0f * kGeluC * fmaf(kGeluA * g * g, g, g));
+}
+
+// act(g) and act'(g)
+__device__ __forceinline__ float2 act_grad(float g, int act) {
+  if (act == ACT_SILU) {
+    const float p = 1.0f / (1.0f + __expf(-g));
+    return make_float2(g * p, p * fmaf(g, 1.0f - p, 1.0f));
+  }
+  if (act == ACT_GELU) {
+    const float c = normcdff(g);
+    return make_float2(g * c, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), c));
+  }
+  // past |g| = 30 p is 0 or 1 to the last bit: the clamp only keeps the cube finite
+  const float c = fminf(fmaxf(g, -30.0f), 30.0f);
+  const float p = 1.0f / (1.0f + __expf(-2.0f * kGeluC * fmaf(kGeluA * c * c, c, c)));
+  return make_float2(g * p, fmaf(2.0f * p * (1.0f - p), kGeluC * fmaf(3.0f * kGeluA * c * c, c, c), p));
+}
+
+// ---------------------------------------------------------------- many rows
+
+// What a launch of the pair kernel forms:
+//   PAIR_GATED  h = act(x Wg^T) (x Wu^T): the 256 accumulator columns of a
+//               tile are 128 hidden units' gate columns, then the same
+//               units' up columns.  In cta_group::2 each CTA stages half of
+//               the B rows: the leader stages Wg's, the peer Wu's.
+//   PAIR_I8     (a b^T) sa sb
+//   PAIR_DX     dg Wg + du Wu: one K loop over both segments; B is read
+//               MN-major (the weights as they lie)
+//   PAIR_DW     dg^T x and du^T x (z = 0, 1): both operands MN-major
+enum : int { PAIR_GATED = 0, PAIR_I8 = 1, PAIR_DX = 2, PAIR_DW = 3 };
+
+constexpr int kPairBoxBytes = 32 * 128;  // an epilogue warp's staging box: 32 rows of 128 bytes
+
+struct PairParams {
+  CUtensorMap tmA;     // K-major: (k, row, seg) box 128 bytes x 128; MN-major: (row, k, z) box 64 x 64
+  CUtensorMap tmB[2];  // K-major: (k, col) box 128 bytes x 128; MN-major: (col, k) box 64 x 64
+  CUtensorMap tmO[3];  // outputs (col, row), box 128 bytes x 32
+  void* out[3];        // PAIR_GATED: h, gate, up (the last two may be null); PAIR_DW: dWg, dWu
+  long long ldo[3];    // in elements
+  const float *sa, *sb;
+  int M, N;            // output rows and columns (PAIR_GATED: hidden units)
+  int nk, segs;        // K stages a segment, segments
+  int tiles_m, tiles_n, total;
+  int band;            // tile rows walked together (see pair_tile)
+  int odt;             // output type
+  int tma_out;         // outputs leave by bulk tensor stores (else lane stores)
+  int act;
+  uint32_t idesc;
+  int* err;
+  unsigned long long timeout_ns;
+};
+
+struct PairTile {
+  int z, tm, tn;
+};
+
+// Tiles in bands of `band` tile rows, column by column inside a band: the
+// tiles that the pairs work on at once share `band` row blocks of A and a
+// few column blocks of B, which stay in L2.
+__device__ __forceinline__ PairTile pair_tile(const PairParams& p, int t) {
+  const int per = p.tiles_m * p.tiles_n;
+  const int z = t / per;
+  int r = t - z * per;
+  const int g0 = r / (p.band * p.tiles_n) * p.band;
+  r -= g0 * p.tiles_n;
+  const int gh = min(p.band, p.tiles_m - g0);
+  return {z, g0 + r % gh, r / gh};
+}
+
+// One staged box of a warp: 32 rows x 128 bytes, 16-byte piece i of row r at
+// piece i ^ (r & 7) (the tensor map's 128-byte swizzle; conflict-free when
+// each lane writes a piece of its own row).
+__device__ __forceinline__ void box_put16(uint8_t* box, int lane, int j, const float (&v)[32], int dt) {
+  uint32_t h[16];
+  pack16(v, dt, h);
+  uint8_t* rowp = box + lane * 128;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(rowp + 16 * ((4 * j + i) ^ (lane & 7))) =
+        make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+}
+
+__device__ __forceinline__ void box_put32(uint8_t* box, int lane, const float (&v)[32]) {
+  uint8_t* rowp = box + lane * 128;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(rowp + 16 * (i ^ (lane & 7))) =
+        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// Sends a staged box to output o at (row0, col0), clipped to M x N.
+__device__ __forceinline__ void box_send(const PairParams& p, int o, uint8_t* box, int lane, int row0, int col0) {
+  if (p.tma_out) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(&p.tmO[o], box, col0, row0, 0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  __syncwarp();
+  const int es = dtype_size(p.odt), w = 128 / es;
+  const int rows = min(32, p.M - row0), cols = min(w, p.N - col0);
+  for (int r = 0; r < rows; ++r) {
+    char* dst = static_cast<char*>(p.out[o]) + ((row0 + r) * p.ldo[o] + col0) * es;
+    for (int c = lane; c < cols; c += 32) {
+      const int at = c * es;
+      const uint8_t* src = box + r * 128 + 16 * ((at >> 4) ^ (r & 7)) + (at & 15);
+      if (es == 2)
+        *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(src);
+      else
+        *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(src);
+    }
+  }
+  __syncwarp();
+}
+
+// The box may be written again: its last bulk store has read it.
+__device__ __forceinline__ void box_free(const PairParams& p, int lane) {
+  if (p.tma_out && lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+
+__device__ __forceinline__ void tmem_block(uint32_t taddr, float (&v)[32]) {
+  uint32_t raw[32];
+  tmem_ld_32x32b_x32(taddr, raw);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[i]);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    dense_pair_kernel(const __grid_constant__ PairParams p) {
+  constexpr bool kI8 = MODE == PAIR_I8;
+  constexpr bool kAmn = MODE == PAIR_DW;
+  constexpr bool kBmn = MODE == PAIR_DX || MODE == PAIR_DW;
+  constexpr int kBke = kI8 ? 128 : 64;                    // K elements a stage
+  constexpr int kCols = MODE == PAIR_GATED ? 128 : kBN;   // output columns a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kStages * kATileBytes;
+  uint8_t* sOut = sB + kStages * kBTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + kEpiWarps * kPairBoxBytes);
+  uint64_t* full = bars;                 // leader: both CTAs' loads of a stage landed
+  uint64_t* empty = bars + kStages;      // both: the MMAs reading a stage finished
+  uint64_t* tfull = bars + 2 * kStages;  // both: accumulator ready
+  uint64_t* tempty = tfull + 2;          // leader: both epilogues drained an accumulator
+  uint64_t* drain = tempty + 2;          // leader: every issued MMA finished
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + kNumBarriers);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int num_pairs = gridDim.x >> 1;
+  const uint64_t limit = p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB[0]);
+    tma_prefetch_desc(&p.tmB[1]);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are initialised before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  const int steps = p.nk * p.segs;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs, warp-converged)
+    int stage = 0;
+    uint32_t phase = 0, used = 0, last_phase = 0;
+    bool ok = true;
+    const void* tmA = &p.tmA;
+    for (int t = pair; ok && t < p.total; t += num_pairs) {
+      const PairTile tc = pair_tile(p, t);
+      const int arow = tc.tm * kBM + static_cast<int>(rank) * kHalfM;
+      const int bcol = MODE == PAIR_GATED ? tc.tn * kCols : tc.tn * kBN + static_cast<int>(rank) * kHalfN;
+      int seg = 0, kb = 0;
+      for (int step = 0; step < steps; ++step) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, s_abort, p.err, limit))) {
+          ok = false;
+          break;
+        }
+        if (leader) mbar_arrive_expect_tx_w(&full[stage], 2u * kStageBytes);
+        const uint32_t fbar = mapa_shared(smem_u32(&full[stage]), 0);
+        uint8_t* a_dst = sA + stage * kATileBytes;
+        uint8_t* b_dst = sB + stage * kBTileBytes;
+        const int k0 = kb * kBke;
+        const void* tmB = &p.tmB[MODE == PAIR_GATED ? rank : (MODE == PAIR_DX ? seg : 0)];
+        if (kAmn) {
+          tma_load_3d_pair_w(a_dst, tmA, fbar, arow, k0, tc.z);
+          tma_load_3d_pair_w(a_dst + 8192, tmA, fbar, arow + 64, k0, tc.z);
+        } else {
+          tma_load_3d_pair_w(a_dst, tmA, fbar, k0, arow, seg);
+        }
+        if (kBmn) {
+          tma_load_3d_pair_w(b_dst, tmB, fbar, bcol, k0, 0);
+          tma_load_3d_pair_w(b_dst + 8192, tmB, fbar, bcol + 64, k0, 0);
+        } else {
+          tma_load_3d_pair_w(b_dst, tmB, fbar, k0, bcol, 0);
+        }
+        used |= 1u << stage;
+        last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++kb == p.nk) {
+          kb = 0;
+          ++seg;
+        }
+      }
+    }
+    // never leave with copies still landing (see gemm_sm100.cuh)
+    if (leader && lane == 0)
+      for (int s = 0; s < kStages; ++s)
+        if ((used >> s) & 1u) wait_bounded(&full[s], (last_phase >> s) & 1u, nullptr, p.err, limit);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader, warp-converged)
+    if (leader) {
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      const uint32_t idesc = p.idesc;
+      const uint64_t dA = kAmn ? smem_desc_sw128(smem_u32(sA), 8192, 1024) : smem_desc_sw128(smem_u32(sA), 16, 1024);
+      const uint64_t dB = kBmn ? smem_desc_sw128(smem_u32(sB), 8192, 1024) : smem_desc_sw128(smem_u32(sB), 16, 1024);
+      constexpr uint32_t ka = kAmn ? 2048 >> 4 : 32 >> 4, kb = kBmn ? 2048 >> 4 : 32 >> 4;
+      for (int t = pair; t < p.total; t += num_pairs) {
+        if (!__all_sync(0xFFFFFFFFu, wait_bounded(&tempty[buf], bphase ^ 1u, s_abort, p.err, limit))) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kBN);
+        for (int step = 0; step < steps; ++step) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(&full[stage], phase, s_abort, p.err, limit))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = dA + static_cast<uint64_t>((stage * kATileBytes) >> 4);
+          const uint64_t db = dB + static_cast<uint64_t>((stage * kBTileBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = (step | kk) != 0 ? 1u : 0u;
+            if (kI8)
+              umma_i8_pair_w(d_tmem, da + kk * ka, db + kk * kb, idesc, acc);
+            else
+              umma_f16_pair_w(d_tmem, da + kk * ka, db + kk * kb, idesc, acc);
+          }
+          umma_commit_pair_mc_w(&empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_mc_w(&tfull[buf], 0x3);
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1u;
+      }
+      umma_commit_pair_mc_w(drain, 0x1);  // every MMA issued so far finishes before TMEM is released
+      if (lane == 0) wait_bounded(drain, 0, nullptr, p.err, limit);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int q = warp & 3;       // TMEM lane quarter
+    const int ew = warp - 2;
+    const int half = ew >> 2;     // which half of the tile's columns
+    uint8_t* box = sOut + ew * kPairBoxBytes;
+    const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    int buf = 0;
+    uint32_t bphase = 0;
+    for (int t = pair; t < p.total; t += num_pairs) {
+      const PairTile tc = pair_tile(p, t);
+      const int row0 = tc.tm * kBM + static_cast<int>(rank) * kHalfM + q * 32;
+      const int col0 = tc.tn * kCols + half * (kCols / 2);
+      float sa = 0.0f;
+      if (kI8 && row0 + lane < p.M) sa = p.sa[row0 + lane];
+      int ok = 1;
+      if (lane == 0) ok = wait_bounded(&tfull[buf], bphase, s_abort, p.err, limit) ? 1 : 0;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                            static_cast<uint32_t>(buf * kBN + half * (kCols / 2));
+      if (row0 < p.M && col0 < p.N) {
+        if (MODE == PAIR_GATED) {
+          // 64 hidden units: the gate's and the up projection's columns lie
+          // 128 apart in this lane's accumulator row
+          box_free(p, lane);
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            float g[32], u[32];
+            tmem_block(acc0 + j * 32, g);
+            tmem_block(acc0 + 128 + j * 32, u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] *= act_of(g[i], p.act);
+            box_put16(box, lane, j, u, p.odt);
+          }
+          box_send(p, 0, box, lane, row0, col0);
+#pragma unroll 1
+          for (int o = 1; o < 3 && p.out[1] != nullptr; ++o) {
+            box_free(p, lane);
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+              float v[32];
+              tmem_block(acc0 + (o - 1) * 128 + j * 32, v);
+              box_put16(box, lane, j, v, p.odt);
+            }
+            box_send(p, o, box, lane, row0, col0);
+          }
+        } else {
+          const int per = p.odt == DT_FP32 ? 1 : 2;  // 32-column blocks a box
+#pragma unroll 1
+          for (int j = 0; j < 4 && col0 + 32 * j < p.N; j += per) {
+            box_free(p, lane);
+#pragma unroll 1
+            for (int i2 = 0; i2 < per; ++i2) {
+              float v[32];
+              tmem_block(acc0 + (j + i2) * 32, v);
+              if (kI8) {
+                // the int32 sum is exact; one rounding to fp32, one for each scale
+                const int c = col0 + (j + i2) * 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float sb = c + i < p.N ? __ldg(p.sb + c + i) : 0.0f;
+                  v[i] = static_cast<float>(__float_as_int(v[i])) * sa * sb;
+                }
+              }
+              if (p.odt == DT_FP32)
+                box_put32(box, lane, v);
+              else
+                box_put16(box, lane, i2, v, p.odt);
+            }
+            box_send(p, MODE == PAIR_DW ? tc.z : 0, box, lane, row0, col0 + 32 * j);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
+      buf ^= 1;
+      if (buf == 0) bphase ^= 1u;
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync_all();  // no CTA of the pair leaves while the other may still signal it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+constexpr int kPairSmemBytes =
+    1024 + kStages * kStageBytes + kEpiWarps * kPairBoxBytes + kNumBarriers * 8 + 16;
+
+// ---------------------------------------------------------------- few rows
+
+// out^T = W x^T: 128 weight rows a CTA are the M operand (gated: 64 hidden
+// units' gate rows, then the same units' up rows), bn tokens the N operand.
+// gridDim.x = splits * weight tiles, a cluster being the splits of one tile;
+// gridDim.y = token tiles.
+struct StreamParams {
+  CUtensorMap tmW[2];  // (k, row), box 128 bytes x 128 (gated: x 64, of Wg and Wu)
+  CUtensorMap tmX;     // (k, token), box 128 bytes x bn
+  void* out[3];        // gated: h, gate, up (the last two may be null)
+  long long ldo[3];
+  const float *sx, *sw;  // int8: a scale a token and a weight row
+  int tokens, N;         // rows and columns of the output
+  int nk, splits, bn, stages, tmem_cols;
+  int odt, vec_out;      // vec_out: four output columns can be stored at once
+  int act;
+  uint32_t idesc;
+  int* err;
+  unsigned long long timeout_ns;
+};
+
+constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
+constexpr int kStreamMaxStages = 12;
+constexpr int kStreamATile = 128 * kRowBytes;
+__host__ __device__ inline int stream_stage_bytes(int bn) { return kStreamATile + bn * kRowBytes; }
+__host__ __device__ inline int stream_smem_bytes(int bn, int stages) {
+  return 1024 + stages * stream_stage_bytes(bn) + (2 * kStreamMaxStages + 1) * 8 + 16;
+}
+
+__device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store4(void* base, long long at, int dt, bool vec, int n, const float (&v)[4]) {
+  char* p = static_cast<char*>(base) + at * dtype_size(dt);
+  if (vec && n >= 4) {
+    if (dt == DT_FP32) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (dt == DT_BF16) {
+          __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<uint32_t*>(&h);
+        } else {
+          __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<uint32_t*>(&h);
+        }
+      }
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+    return;
+  }
+  for (int i = 0; i < 4 && i < n; ++i) store_elem(p + i * dtype_size(dt), dt, v[i]);
+}
+
+template <bool I8, bool GATED>
+__global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr int kBke = I8 ? 128 : 64;
+  constexpr int kUnits = GATED ? 64 : 128;  // output columns a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage_bytes = stream_stage_bytes(p.bn);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
+  uint64_t* empty = full + kStreamMaxStages;
+  uint64_t* done = empty + kStreamMaxStages;  // every MMA of the tile finished
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = static_cast<int>(cluster_ctarank());
+  const int tile = blockIdx.x / p.splits;
+  const int unit0 = tile * kUnits;
+  const int tok0 = blockIdx.y * p.bn;
+  const uint64_t limit = p.timeout_ns;
+  // this CTA's K stages
+  const int kbeg = static_cast<int>(static_cast<long long>(p.nk) * split / p.splits);
+  const int kend = static_cast<int>(static_cast<long long>(p.nk) * (split + 1) / p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, p.tmem_cols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&p.tmW[0]);
+    if (GATED) tma_prefetch_desc(&p.tmW[1]);
+    tma_prefetch_desc(&p.tmX);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0, used = 0, last_phase = 0;
+    for (int kb = kbeg; kb < kend; ++kb) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, s_abort, p.err, limit))) break;
+      uint8_t* dst = smem + stage * stage_bytes;
+      mbar_arrive_expect_tx_w(&full[stage], static_cast<uint32_t>(stage_bytes));
+      const int k0 = kb * kBke;
+      if (GATED) {
+        tma_load_3d_w(dst, &p.tmW[0], &full[stage], k0, unit0, 0);
+        tma_load_3d_w(dst + kStreamATile / 2, &p.tmW[1], &full[stage], k0, unit0, 0);
+      } else {
+        tma_load_3d_w(dst, &p.tmW[0], &full[stage], k0, unit0, 0);
+      }
+      tma_load_3d_w(dst + kStreamATile, &p.tmX, &full[stage], k0, tok0, 0);
+      used |= 1u << stage;
+      last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    // no copy is still landing when the stages are used again below
+    if (lane == 0)
+      for (int s = 0; s < p.stages; ++s)
+        if ((used >> s) & 1u) wait_bounded(&full[s], (last_phase >> s) & 1u, nullptr, p.err, limit);
+  } else if (warp == 1) {
+    int stage = 0;
+    uint32_t phase = 0;
+    const uint64_t d0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    for (int kb = kbeg; kb < kend; ++kb) {
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(&full[stage], phase, s_abort, p.err, limit))) break;
+      tc_fence_after();
+      const uint64_t da = d0 + static_cast<uint64_t>((stage * stage_bytes) >> 4);
+      const uint64_t db = da + static_cast<uint64_t>(kStreamATile >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint32_t acc = (kb > kbeg || kk > 0) ? 1u : 0u;
+        if (I8)
+          umma_i8_w(tmem_base, da + 2 * kk, db + 2 * kk, p.idesc, acc);
+        else
+          umma_f16_w(tmem_base, da + 2 * kk, db + 2 * kk, p.idesc, acc);
+      }
+      umma_commit_w(&empty[stage]);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    umma_commit_w(done);
+    if (lane == 0) wait_bounded(done, 0, nullptr, p.err, limit);
+    tc_fence_before();
+  }
+  __syncwarp();
+  __syncthreads();  // the MMAs are done and no copy is in flight: the stages hold the partial sums from here on
+  float* part = reinterpret_cast<float*>(smem);  // [bn tokens][128 weight rows]
+  const int toks = min(p.bn, p.tokens - tok0);
+  if (warp >= 2) {
+    tc_fence_after();
+    const int q = warp & 3;
+    const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    for (int c = 0; c < toks; c += 16) {
+      uint32_t raw[16];
+      tmem_ld_32x32b_x16(acc0 + c, raw);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        part[(c + i) * 128 + q * 32 + lane] = __uint_as_float(raw[i]);  // int8: the int32 bits
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();
+  // Join the splits in their order (int8: whole numbers) and store: four
+  // consecutive units of one token a thread, a token's units side by side.
+  constexpr int kQuads = kUnits / 4;
+  const uint32_t part0 = smem_u32(part);
+  const int items = toks * kQuads;
+  for (int i = split * kStreamThreads + threadIdx.x; i < items; i += p.splits * kStreamThreads) {
+    const int tok = i / kQuads, c = (i - tok * kQuads) * 4;
+    if (unit0 + c >= p.N) continue;
+    const uint32_t at = part0 + static_cast<uint32_t>(tok * 128 + c) * 4u;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int iv[4] = {0, 0, 0, 0};
+    for (int s = 0; s < p.splits; ++s) {
+      const uint32_t remote = mapa_shared(at, s);
+      const float4 f = ld_dsmem_f4(remote);
+      if (I8) {
+        iv[0] += __float_as_int(f.x), iv[1] += __float_as_int(f.y);
+        iv[2] += __float_as_int(f.z), iv[3] += __float_as_int(f.w);
+      } else {
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+      }
+      if (GATED) {
+        const float4 g = ld_dsmem_f4(remote + 64 * 4);
+        u[0] += g.x, u[1] += g.y, u[2] += g.z, u[3] += g.w;
+      }
+    }
+    const int n = p.N - (unit0 + c);
+    const long long tk = tok0 + tok;
+    if (I8) {
+      const float sx = p.sx[tk];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = j < n ? static_cast<float>(iv[j]) * sx * p.sw[unit0 + c + j] : 0.0f;
+    }
+    if (GATED) {
+      float h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = act_of(v[j], p.act) * u[j];
+      store4(p.out[0], tk * p.ldo[0] + unit0 + c, p.odt, p.vec_out, n, h);
+      if (p.out[1] != nullptr) {
+        store4(p.out[1], tk * p.ldo[1] + unit0 + c, p.odt, p.vec_out, n, v);
+        store4(p.out[2], tk * p.ldo[2] + unit0 + c, p.odt, p.vec_out, n, u);
+      }
+    } else {
+      store4(p.out[0], tk * p.ldo[0] + unit0 + c, p.odt, p.vec_out, n, v);
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // no CTA leaves while another may read its part
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------- around the products
+
+// Rows of `cols` elements copied to rows of ld_out elements (a 16-byte
+// multiple), the rest zero: what a tensor map needs where the caller's rows
+// do not start on 16-byte boundaries.  U: the element as a whole number.
+template <typename U>
+__global__ void __launch_bounds__(256) pad_rows_kernel(const U* in, long long ld_in, U* out, long long ld_out,
+                                                       long long rows, int cols) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = 16 / sizeof(U);
+  const long long per = ld_out / V;
+  const long long total = rows * per;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 256ll * gridDim.x) {
+    const long long r = i / per;
+    const int c = static_cast<int>(i - r * per) * V;
+    union {
+      uint4 v;
+      U e[V];
+    } o;
+    const U* src = in + r * ld_in + c;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o.e[j] = c + j < cols ? src[j] : U(0);
+    *reinterpret_cast<uint4*>(out + r * ld_out + c) = o.v;
+  }
+}
+
+// dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
+// rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
+// io type here, as the operands of the products that follow.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) gated_dact_kernel(const T* dh, long long ldh, const T* gate, long long ldg,
+                                                         const T* up, long long ldu, T* out, long long ldp,
+                                                         long long rows, int cols, int act) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = VEC ? Elem<T>::vec : 1;
+  const long long zs = rows * ldp;
+  const long long per = (cols + V - 1) / V;
+  const long long total = rows * per;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 256ll * gridDim.x) {
+    const long long r = i / per;
+    const int c = static_cast<int>(i - r * per) * V;
+    T* o = out + r * ldp + c;  // dg; du lies zs further
+    if (VEC) {
+      float d[Elem<T>::vec], g[Elem<T>::vec], u[Elem<T>::vec];
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(dh + r * ldh + c), d);
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(gate + r * ldg + c), g);
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(up + r * ldu + c), u);
+#pragma unroll
+      for (int j = 0; j < Elem<T>::vec; ++j) {
+        const float2 a = act_grad(g[j], act);
+        g[j] = d[j] * u[j] * a.y;
+        d[j] = d[j] * a.x;
+      }
+      *reinterpret_cast<uint4*>(o) = Elem<T>::pack(g);
+      *reinterpret_cast<uint4*>(o + zs) = Elem<T>::pack(d);
+    } else {
+      const float d = Elem<T>::get(dh[r * ldh + c]);
+      const float2 a = act_grad(Elem<T>::get(gate[r * ldg + c]), act);
+      o[0] = Elem<T>::put(d * Elem<T>::get(up[r * ldu + c]) * a.y);
+      o[zs] = Elem<T>::put(d * a.x);
+    }
+  }
+}
+
+}  // namespace msb

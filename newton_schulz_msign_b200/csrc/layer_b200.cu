@@ -1,0 +1,726 @@
+// layer_b200.cu - C ABI of the layer operators around the Muon step
+// (declared in include/msign_b200.h): RMS norm with its int8 output and its
+// gradients, the gated feed-forward block with its gradients, and the int8
+// product with scales.  Argument checks, workspace layout, tensor maps and
+// launches; the kernels are in norm_sm100.cuh and dense_sm100.cuh.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "dense_sm100.cuh"
+#include "host_sm100.cuh"
+#include "msign_b200.h"
+#include "norm_sm100.cuh"
+
+namespace msb {
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+// int8 products: |a b| <= 2^14, so K < 2^17 keeps every int32 sum exact
+constexpr int64_t kMaxI8K = (int64_t(1) << 17) - 1;
+constexpr int kPlanSms = 148;  // launch plans must not depend on the device: workspace sizes are host-only queries
+
+// Launch with the programmatic-dependent attribute (every kernel here waits
+// for its predecessor before it touches memory) and, where cluster > 0, that
+// cluster width.
+template <typename... KArgs, typename... Args>
+msign_status launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, int kind, double flops,
+                    double bytes, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
+  if (cluster > 0) {
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cfg.attrs = at;
+  prof_begin(stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  prof_end(kind, stream, flops, bytes);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MSIGN_ERR_CUDA;
+  }
+  return MSIGN_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
+
+// A row stride argument: 0 means rows back to back.
+int64_t stride_of(int64_t stride, int64_t cols) { return stride > 0 ? stride : cols; }
+bool valid_stride(int64_t stride, int64_t cols) { return stride == 0 || stride >= cols; }
+
+// Rows that 16-byte accesses reach: an aligned base, and a stride of whole
+// 16-byte pieces where there is more than one row.
+bool rows_aligned(const void* p, int64_t stride, int64_t rows, int es) {
+  return aligned16(p) && (rows <= 1 || (stride * es) % 16 == 0);
+}
+
+// ---------------------------------------------------------------- RMS norm
+
+struct NormPlan {
+  bool vec = false;
+  int vpt = 0;
+  dim3 block;
+};
+
+// Threads for rows of `pieces` 16-byte pieces: up to 128 pieces a warp takes
+// a row (no block barrier), beyond that a block does.
+NormPlan norm_plan(int64_t pieces, int rows_per_block, int block_vpt, int max_threads, int max_vpt) {
+  NormPlan p;
+  if (pieces <= 32 * kNormVpt) {
+    p.vec = true;
+    p.vpt = pieces <= 32 ? 1 : pieces <= 64 ? 2 : 4;
+    p.block = dim3(32, rows_per_block);
+    return p;
+  }
+  int vpt = block_vpt;
+  while (vpt < max_vpt && pieces > int64_t(max_threads) * vpt) vpt *= 2;
+  if (pieces > int64_t(max_threads) * vpt) return p;
+  p.vec = true;
+  p.vpt = vpt;
+  p.block = dim3(static_cast<unsigned>(round_up(ceil_div(pieces, vpt), 32)), 1);
+  return p;
+}
+
+template <typename T, bool Q8>
+msign_status norm_run(const NormArgs& a, bool vec_ok, double bytes, cudaStream_t stream) {
+  NormPlan p;
+  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec, 4, 2, kNormMaxThreads, kNormVpt);
+  if (!p.vec)
+    return launch(rms_norm_loop_kernel<T, Q8>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
+                  stream, a);
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, p.block.y)));
+  auto* k = p.vpt == 1 ? rms_norm_kernel<T, 1, Q8> : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8> : rms_norm_kernel<T, 4, Q8>;
+  return launch(k, grid, p.block, 0, 0, 3, 0.0, bytes, stream, a);
+}
+
+msign_status norm_call(const void* x, const void* residual, const void* weight, void* y, void* sum_out, float* scale,
+                       msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                       int64_t r_stride, int64_t y_stride, int64_t s_stride, float eps, msign_stream_t stream) {
+  const bool q8 = scale != nullptr;
+  if (!valid_dtype(io_dtype) || !valid_dtype(w_dtype)) return MSIGN_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f) || !std::isfinite(eps)) return MSIGN_ERR_INVALID_ARG;
+  if (!valid_stride(x_stride, cols) || !valid_stride(r_stride, cols) || !valid_stride(y_stride, cols) ||
+      !valid_stride(s_stride, cols))
+    return MSIGN_ERR_INVALID_ARG;
+  if (residual == nullptr && sum_out != nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (weight != nullptr && w_dtype != io_dtype && w_dtype != MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
+  if (rows == 0 || cols == 0) return MSIGN_OK;
+  if (x == nullptr || y == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  DeviceState* dev = nullptr;
+  msign_status st = device_state(&dev);
+  if (st != MSIGN_OK) return st;
+  NormArgs a = {};
+  a.x = x, a.r = residual, a.w = weight, a.y = y, a.s = sum_out, a.scale = scale;
+  a.xs = stride_of(x_stride, cols), a.rs = stride_of(r_stride, cols);
+  a.ys = stride_of(y_stride, cols), a.ss = stride_of(s_stride, cols);
+  a.rows = rows, a.cols = static_cast<int>(cols), a.eps = eps;
+  a.w_f32 = w_dtype == MSIGN_FP32;
+  const int dt = to_dt(io_dtype), es = dtype_size(dt), v = 16 / es;
+  bool vec = cols % v == 0 && rows_aligned(x, a.xs, rows, es) && (weight == nullptr || aligned16(weight)) &&
+             (residual == nullptr || rows_aligned(residual, a.rs, rows, es)) &&
+             (sum_out == nullptr || rows_aligned(sum_out, a.ss, rows, es));
+  vec = vec && (q8 ? reinterpret_cast<uintptr_t>(y) % v == 0 && (rows <= 1 || a.ys % v == 0)
+                   : rows_aligned(y, a.ys, rows, es));
+  const double e = static_cast<double>(rows) * cols;
+  const double bytes = e * es * (1 + (residual != nullptr) + (sum_out != nullptr)) + e * (q8 ? 1 : es);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dt == DT_BF16)
+    return q8 ? norm_run<__nv_bfloat16, true>(a, vec, bytes, s) : norm_run<__nv_bfloat16, false>(a, vec, bytes, s);
+  if (dt == DT_FP16) return q8 ? norm_run<__half, true>(a, vec, bytes, s) : norm_run<__half, false>(a, vec, bytes, s);
+  return q8 ? norm_run<float, true>(a, vec, bytes, s) : norm_run<float, false>(a, vec, bytes, s);
+}
+
+// Partial rows of dw that the gradients leave at most: four blocks an SM.
+constexpr int64_t kDwParts = 4 * kPlanSms;
+constexpr int64_t kDwLoopParts = 128;  // row chunks of the loop form
+
+template <typename T>
+msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char* ws, double bytes,
+                          cudaStream_t stream) {
+  Carver cv(ws);
+  float* part = static_cast<float*>(cv.take(sizeof(float) * std::min<int64_t>(a.rows, kDwParts) * a.cols));
+  float* rstd = static_cast<float*>(cv.take(sizeof(float) * a.rows));
+  NormPlan p;
+  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec, 8, 1, kNormBwdThreads, kNormVpt);
+  a.part = dw != nullptr ? part : nullptr;
+  int64_t parts;
+  msign_status st;
+  if (p.vec) {
+    const int threads = static_cast<int>(p.block.x * p.block.y);
+    parts = std::min<int64_t>(ceil_div(a.rows, p.block.y),
+                              int64_t(kPlanSms) * std::max(1, std::min(4, 1024 / threads)));
+    const size_t smem = p.block.y > 1 && dw != nullptr ? sizeof(float) * p.block.y * a.cols : 0;
+    auto* k = p.vpt == 1 ? rms_norm_bwd_kernel<T, 1> : p.vpt == 2 ? rms_norm_bwd_kernel<T, 2> : rms_norm_bwd_kernel<T, 4>;
+    st = launch(k, dim3(static_cast<unsigned>(parts)), p.block, smem, 0, 3, 0.0, bytes, stream, a);
+    if (st != MSIGN_OK) return st;
+  } else {
+    a.rstd = dw != nullptr ? rstd : nullptr;
+    st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
+                stream, a);
+    if (st != MSIGN_OK || dw == nullptr) return st;
+    const int chunk = static_cast<int>(ceil_div(a.rows, std::min<int64_t>(a.rows, kDwLoopParts)));
+    parts = ceil_div(a.rows, chunk);
+    st = launch(rms_norm_dw_loop_kernel<T>,
+                dim3(static_cast<unsigned>(ceil_div(a.cols, 128)), static_cast<unsigned>(parts)), dim3(128), 0, 0, 3,
+                0.0, 0.0, stream, a, chunk);
+    if (st != MSIGN_OK) return st;
+  }
+  if (dw == nullptr) return MSIGN_OK;
+  return launch(dw_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(a.cols, 32))), dim3(32, 32), 0, 0, 3, 0.0,
+                4.0 * parts * a.cols, stream, static_cast<const float*>(part), static_cast<int>(parts), a.cols, dw,
+                dw_dt);
+}
+
+// ---------------------------------------------------------------- products
+
+CUtensorMapDataType tma_type(int dt, bool i8) {
+  if (i8) return CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return dt == DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+         : dt == DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+}
+
+// Tensor map of rows x cols elements (es bytes each, row stride ld), `z` of
+// them zs elements apart, in the 128-byte swizzle.  Elements of a box beyond
+// the extents read as 0 and are not written.
+bool map_rows(CUtensorMap* tm, const void* p, CUtensorMapDataType type, int es, int64_t rows, int64_t cols, int64_t ld,
+              int box_cols, int box_rows, int64_t z = 1, int64_t zs = 0, bool out = false) {
+  const int64_t row_bytes = rows > 1 || z > 1 ? ld * es : round_up(cols * es, 16);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(z)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                           static_cast<cuuint64_t>(z > 1 ? zs * es : row_bytes * rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return g_encode(tm, type, 3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B,
+                  out ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand's rows as a tensor map takes them: where they lie, or copied
+// into the workspace with rows of whole 16-byte pieces.
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+  int es;
+  bool direct() const { return rows_aligned(p, ld, rows, es); }
+  int64_t padded_ld() const { return round_up(cols, 16 / es); }
+  size_t padded_bytes() const { return static_cast<size_t>(rows) * padded_ld() * es; }
+};
+
+void carve_operand(Carver& cv, const Operand& o, void** copy) { *copy = o.direct() ? nullptr : cv.take(o.padded_bytes()); }
+
+msign_status place_operand(Operand* o, void* copy, cudaStream_t stream) {
+  if (copy == nullptr) return MSIGN_OK;
+  const int64_t ldp = o->padded_ld();
+  const int64_t pieces = o->rows * (ldp * o->es / 16);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(pieces, 256), 16 * kPlanSms)));
+  const double bytes = 2.0 * o->rows * o->cols * o->es;
+  const msign_status st =
+      o->es == 1 ? launch(pad_rows_kernel<uint8_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes, stream,
+                          static_cast<const uint8_t*>(o->p), o->ld, static_cast<uint8_t*>(copy), ldp, o->rows,
+                          static_cast<int>(o->cols))
+                 : launch(pad_rows_kernel<uint16_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes, stream,
+                          static_cast<const uint16_t*>(o->p), o->ld, static_cast<uint16_t*>(copy), ldp, o->rows,
+                          static_cast<int>(o->cols));
+  o->p = copy;
+  o->ld = ldp;
+  return st;
+}
+
+// Instruction descriptor: D type (fp32 or int32), A and B types, which of
+// them is read MN-major, N and M of the MMA.
+uint32_t make_idesc(int dt, bool i8, bool a_mn, bool b_mn, int n, int m) {
+  const uint32_t fmt = i8 ? 1u : (dt == DT_BF16 ? 1u : 0u);  // signed int8; bf16 or fp16
+  return ((i8 ? 2u : 1u) << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+template <int MODE>
+msign_status pair_setup() {
+  return cudaFuncSetAttribute(dense_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmemBytes) ==
+                 cudaSuccess
+             ? MSIGN_OK
+             : MSIGN_ERR_CUDA;
+}
+
+template <bool I8, bool GATED>
+msign_status stream_setup() {
+  return cudaFuncSetAttribute(dense_stream_kernel<I8, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) ==
+                 cudaSuccess
+             ? MSIGN_OK
+             : MSIGN_ERR_CUDA;
+}
+
+std::mutex g_layer_mu;
+bool g_layer_ready[64] = {};
+
+// The device's state, with the product kernels' shared memory limits raised.
+msign_status layer_state(DeviceState** out) {
+  msign_status st = device_state(out);
+  if (st != MSIGN_OK) return st;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSIGN_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_layer_mu);
+  if (g_layer_ready[dev]) return MSIGN_OK;
+  for (msign_status s : {pair_setup<PAIR_GATED>(), pair_setup<PAIR_I8>(), pair_setup<PAIR_DX>(), pair_setup<PAIR_DW>(),
+                         stream_setup<true, false>(), stream_setup<false, true>()})
+    if (s != MSIGN_OK) return s;
+  g_layer_ready[dev] = true;
+  return MSIGN_OK;
+}
+
+// Outputs o of the pair kernel, M x N each.
+bool pair_outputs(PairParams* p, int n, void* const* out, const int64_t* ld, int odt) {
+  const int es = dtype_size(odt);
+  p->odt = odt;
+  p->tma_out = 1;
+  for (int o = 0; o < n; ++o) {
+    p->out[o] = out[o];
+    p->ldo[o] = ld[o];
+    if (out[o] != nullptr && !rows_aligned(out[o], ld[o], p->M, es)) p->tma_out = 0;
+  }
+  if (p->tma_out)
+    for (int o = 0; o < n; ++o)
+      if (out[o] != nullptr &&
+          !map_rows(&p->tmO[o], out[o], tma_type(odt, false), es, p->M, p->N, ld[o], 128 / es, 32, 1, 0, true))
+        return false;
+  return true;
+}
+
+template <int MODE>
+msign_status pair_launch(PairParams* p, int64_t nz, double flops, double bytes, DeviceState* dev, cudaStream_t stream) {
+  const int cols = MODE == PAIR_GATED ? 128 : kBN;
+  p->tiles_m = static_cast<int>(ceil_div(p->M, kBM));
+  p->tiles_n = static_cast<int>(ceil_div(p->N, cols));
+  const int64_t total = int64_t(p->tiles_m) * p->tiles_n * nz;
+  if (total > INT32_MAX / 2) return MSIGN_ERR_UNSUPPORTED;
+  p->total = static_cast<int>(total);
+  p->band = std::min(8, p->tiles_m);
+  p->err = dev->err;
+  p->timeout_ns = kWaitLimitNs;
+  const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(total, dev->max_pairs));
+  // (the cluster width is compiled into the kernel)
+  return launch(dense_pair_kernel<MODE>, dim3(grid), dim3(kThreads), kPairSmemBytes, 0, 0, flops, bytes, stream, *p);
+}
+
+// Tokens that the stream kernel takes.
+constexpr int64_t kStreamTokens = 256;
+
+template <bool I8, bool GATED>
+msign_status stream_launch(StreamParams* p, double flops, double bytes, DeviceState* dev, cudaStream_t stream) {
+  const int units = GATED ? 64 : 128;
+  const int64_t tiles = ceil_div(p->N, units);
+  if (tiles > INT32_MAX / 16) return MSIGN_ERR_UNSUPPORTED;
+  p->tmem_cols = 32;
+  while (p->tmem_cols < p->bn) p->tmem_cols *= 2;
+  // narrow token tiles: two CTAs an SM
+  const int budget = p->bn <= 64 ? 113 * 1024 : 220 * 1024;
+  p->stages = std::min(kStreamMaxStages, (budget - stream_smem_bytes(p->bn, 0)) / stream_stage_bytes(p->bn));
+  const int64_t slots = p->bn <= 64 ? 2 * kPlanSms : kPlanSms;
+  p->splits = 1;
+  while (p->splits < 8 && tiles * p->splits * 2 <= slots && p->nk >= 8 * p->splits) p->splits *= 2;
+  p->err = dev->err;
+  p->timeout_ns = kWaitLimitNs;
+  return launch(dense_stream_kernel<I8, GATED>, dim3(static_cast<unsigned>(tiles * p->splits), 1),
+                dim3(kStreamThreads), stream_smem_bytes(p->bn, p->stages), p->splits, 0, flops, bytes, stream, *p);
+}
+
+msign_status zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int es, cudaStream_t stream) {
+  if (p == nullptr || rows == 0 || cols == 0) return MSIGN_OK;
+  return cudaMemset2DAsync(p, static_cast<size_t>(ld) * es, 0, static_cast<size_t>(cols) * es,
+                           static_cast<size_t>(rows), stream) == cudaSuccess
+             ? MSIGN_OK
+             : MSIGN_ERR_CUDA;
+}
+
+bool workspace_ok(const void* ws, size_t bytes, size_t need) {
+  return need == 0 || (ws != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(ws) % 256) == 0);
+}
+
+size_t carved(const Carver& cv) { return cv.off == 0 ? 0 : cv.off + 1024; }
+
+char* carve_base(void* ws) { return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 1023) & ~uintptr_t(1023)); }
+
+// ---------------------------------------------------------------- gated feed-forward
+
+struct FfnShape {
+  int64_t t, d, h;
+};
+
+struct FfnCopies {
+  void *x, *wg, *wu, *dgu;
+};
+
+void carve_ffn(Carver& cv, const FfnShape& s, const Operand& x, const Operand& wg, const Operand& wu, bool backward,
+               FfnCopies* c) {
+  carve_operand(cv, x, &c->x);
+  carve_operand(cv, wg, &c->wg);
+  carve_operand(cv, wu, &c->wu);
+  c->dgu = backward ? cv.take(size_t(4) * s.t * round_up(s.h, 8)) : nullptr;
+}
+
+// Checks that the forward and the backward call share.
+msign_status ffn_check(msign_dtype dtype, int act, const FfnShape& s, int64_t x_stride, int64_t w_stride) {
+  if (!valid_dtype(dtype) || act < 0 || act > 2 || s.t < 0 || s.d < 0 || s.h < 0) return MSIGN_ERR_INVALID_ARG;
+  if (!valid_stride(x_stride, s.d) || !valid_stride(w_stride, s.d)) return MSIGN_ERR_INVALID_ARG;
+  if (dtype == MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
+  if (s.t > kMaxDim || s.d > kMaxDim || s.h > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  return MSIGN_OK;
+}
+
+template <typename T>
+msign_status dact_run(const void* dh, int64_t ldh, const void* gate, const void* up, int64_t ldp_in, void* dgu,
+                      const FfnShape& s, int act, cudaStream_t stream) {
+  const int64_t ldp = round_up(s.h, 8);
+  const bool vec = s.h % 8 == 0 && rows_aligned(dh, ldh, s.t, 2) && rows_aligned(gate, ldp_in, s.t, 2) &&
+                   rows_aligned(up, ldp_in, s.t, 2);
+  const int64_t items = s.t * (vec ? s.h / 8 : s.h);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16 * kPlanSms)));
+  auto* k = vec ? gated_dact_kernel<T, true> : gated_dact_kernel<T, false>;
+  return launch(k, grid, dim3(256), 0, 0, 3, 0.0, 10.0 * s.t * s.h, stream, static_cast<const T*>(dh), ldh,
+                static_cast<const T*>(gate), ldp_in, static_cast<const T*>(up), ldp_in, static_cast<T*>(dgu), ldp, s.t,
+                static_cast<int>(s.h), act);
+}
+
+}  // namespace
+
+}  // namespace msb
+
+using namespace msb;
+
+extern "C" {
+
+// ---------------------------------------------------------------- RMS norm
+
+msign_status rms_norm(const void* x, const void* residual, const void* weight, void* y, void* sum_out,
+                      msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols, int64_t x_stride,
+                      int64_t r_stride, int64_t y_stride, int64_t s_stride, float eps, msign_stream_t stream) {
+  return norm_call(x, residual, weight, y, sum_out, nullptr, io_dtype, w_dtype, rows, cols, x_stride, r_stride,
+                   y_stride, s_stride, eps, stream);
+}
+
+msign_status rms_norm_q8(const void* x, const void* residual, const void* weight, int8_t* q, float* scale,
+                         void* sum_out, msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols,
+                         int64_t x_stride, int64_t r_stride, int64_t q_stride, int64_t s_stride, float eps,
+                         msign_stream_t stream) {
+  if (rows > 0 && scale == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (rows > 0 && cols == 0) {
+    if (rows > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+    return cudaMemsetAsync(scale, 0, sizeof(float) * static_cast<size_t>(rows), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MSIGN_OK
+               : MSIGN_ERR_CUDA;
+  }
+  return norm_call(x, residual, weight, q, sum_out, scale, io_dtype, w_dtype, rows, cols, x_stride, r_stride, q_stride,
+                   s_stride, eps, stream);
+}
+
+size_t rms_norm_backward_workspace_size(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  Carver cv(nullptr);
+  cv.take(sizeof(float) * std::min<int64_t>(rows, kDwParts) * cols);
+  cv.take(sizeof(float) * rows);
+  return cv.off + 1024;
+}
+
+msign_status rms_norm_backward(const void* dy, const void* sum, const void* weight, const void* dsum, void* dx,
+                               void* dw, msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols,
+                               int64_t dy_stride, int64_t sum_stride, int64_t dsum_stride, int64_t dx_stride, float eps,
+                               void* workspace, size_t workspace_bytes, msign_stream_t stream) {
+  if (!valid_dtype(io_dtype) || !valid_dtype(w_dtype)) return MSIGN_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f) || !std::isfinite(eps)) return MSIGN_ERR_INVALID_ARG;
+  if (!valid_stride(dy_stride, cols) || !valid_stride(sum_stride, cols) || !valid_stride(dsum_stride, cols) ||
+      !valid_stride(dx_stride, cols))
+    return MSIGN_ERR_INVALID_ARG;
+  if ((weight != nullptr || dw != nullptr) && w_dtype != io_dtype && w_dtype != MSIGN_FP32)
+    return MSIGN_ERR_UNSUPPORTED;
+  if (cols == 0) return MSIGN_OK;
+  if (rows > kMaxDim || cols > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int dt = to_dt(io_dtype), es = dtype_size(dt), v = 16 / es;
+  const int wdt = to_dt(w_dtype);
+  if (rows == 0) return zero_rows(dw, cols, 1, cols, dtype_size(wdt), s);  // a sum over no rows
+  if (dy == nullptr || sum == nullptr || dx == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (dw != nullptr && !workspace_ok(workspace, workspace_bytes, rms_norm_backward_workspace_size(rows, cols)))
+    return MSIGN_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  msign_status st = device_state(&dev);
+  if (st != MSIGN_OK) return st;
+  NormBwdArgs a = {};
+  a.dy = dy, a.z = sum, a.w = weight, a.ds = dsum, a.dz = dx;
+  a.dys = stride_of(dy_stride, cols), a.zs = stride_of(sum_stride, cols);
+  a.dss = stride_of(dsum_stride, cols), a.dzs = stride_of(dx_stride, cols);
+  a.rows = rows, a.cols = static_cast<int>(cols), a.w_f32 = w_dtype == MSIGN_FP32, a.eps = eps;
+  const bool vec = cols % v == 0 && rows_aligned(dy, a.dys, rows, es) && rows_aligned(sum, a.zs, rows, es) &&
+                   rows_aligned(dx, a.dzs, rows, es) && (dsum == nullptr || rows_aligned(dsum, a.dss, rows, es)) &&
+                   (weight == nullptr || aligned16(weight));
+  const double bytes = static_cast<double>(rows) * cols * es * (3 + (dsum != nullptr));
+  char* ws = dw != nullptr ? carve_base(workspace) : nullptr;
+  if (dt == DT_BF16) return norm_bwd_run<__nv_bfloat16>(a, dw, wdt, vec, ws, bytes, s);
+  if (dt == DT_FP16) return norm_bwd_run<__half>(a, dw, wdt, vec, ws, bytes, s);
+  return norm_bwd_run<float>(a, dw, wdt, vec, ws, bytes, s);
+}
+
+// ---------------------------------------------------------------- int8 product
+
+size_t i8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, const int8_t* a, int64_t a_stride, const int8_t* b,
+                                int64_t b_stride) {
+  if (m <= 0 || n <= 0 || k <= 0) return 0;
+  Carver cv(nullptr);
+  void* c;
+  carve_operand(cv, Operand{a, m, k, stride_of(a_stride, k), 1}, &c);
+  carve_operand(cv, Operand{b, n, k, stride_of(b_stride, k), 1}, &c);
+  return carved(cv);
+}
+
+msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, const float* b_scale, void* out,
+                       msign_dtype out_dtype, int64_t m, int64_t n, int64_t k, int64_t a_stride, int64_t b_stride,
+                       int64_t out_stride, void* workspace, size_t workspace_bytes, msign_stream_t stream_) {
+  if (!valid_dtype(out_dtype) || m < 0 || n < 0 || k < 0) return MSIGN_ERR_INVALID_ARG;
+  if (!valid_stride(a_stride, k) || !valid_stride(b_stride, k) || !valid_stride(out_stride, n))
+    return MSIGN_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return MSIGN_OK;
+  if (out == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxI8K) return MSIGN_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int odt = to_dt(out_dtype), oes = dtype_size(odt);
+  const int64_t ldo = stride_of(out_stride, n);
+  if (k == 0) return zero_rows(out, ldo, m, n, oes, stream);
+  if (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes, i8_matmul_workspace_size(m, n, k, a, a_stride, b, b_stride)))
+    return MSIGN_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  msign_status st = layer_state(&dev);
+  if (st != MSIGN_OK) return st;
+  Operand oa{a, m, k, stride_of(a_stride, k), 1}, ob{b, n, k, stride_of(b_stride, k), 1};
+  {
+    Carver cv(carve_base(workspace));
+    void *ca, *cb;
+    carve_operand(cv, oa, &ca);
+    carve_operand(cv, ob, &cb);
+    if ((st = place_operand(&oa, ca, stream)) != MSIGN_OK) return st;
+    if ((st = place_operand(&ob, cb, stream)) != MSIGN_OK) return st;
+  }
+  const double flops = 2.0 * m * n * k;
+  const double bytes = static_cast<double>(m) * k + static_cast<double>(n) * k + static_cast<double>(oes) * m * n;
+  const CUtensorMapDataType type = tma_type(0, true);
+  if (m <= kStreamTokens) {
+    StreamParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.bn = static_cast<int>(round_up(m, 16));
+    if (!map_rows(&p.tmW[0], ob.p, type, 1, n, k, ob.ld, 128, 128) ||
+        !map_rows(&p.tmX, oa.p, type, 1, m, k, oa.ld, 128, p.bn))
+      return MSIGN_ERR_CUDA;
+    p.out[0] = out, p.ldo[0] = ldo;
+    p.sx = a_scale, p.sw = b_scale;
+    p.tokens = static_cast<int>(m), p.N = static_cast<int>(n), p.nk = static_cast<int>(ceil_div(k, 128));
+    p.odt = odt;
+    p.vec_out = reinterpret_cast<uintptr_t>(out) % (4 * oes) == 0 && (m <= 1 || ldo % 4 == 0);
+    p.idesc = make_idesc(0, true, false, false, p.bn, 128);
+    return stream_launch<true, false>(&p, flops, bytes, dev, stream);
+  }
+  PairParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int>(m), p.N = static_cast<int>(n), p.nk = static_cast<int>(ceil_div(k, 128)), p.segs = 1;
+  if (!map_rows(&p.tmA, oa.p, type, 1, m, k, oa.ld, 128, 128) ||
+      !map_rows(&p.tmB[0], ob.p, type, 1, n, k, ob.ld, 128, 128))
+    return MSIGN_ERR_CUDA;
+  p.tmB[1] = p.tmB[0];
+  void* outs[1] = {out};
+  if (!pair_outputs(&p, 1, outs, &ldo, odt)) return MSIGN_ERR_CUDA;
+  p.sa = a_scale, p.sb = b_scale;
+  p.idesc = make_idesc(0, true, false, false, kBN, kBM);
+  return pair_launch<PAIR_I8>(&p, 1, flops, bytes, dev, stream);
+}
+
+// ---------------------------------------------------------------- gated feed-forward
+
+size_t gated_ffn_workspace_size(int64_t tokens, int64_t d, int64_t h, const void* x, int64_t x_stride,
+                                const void* w_gate, const void* w_up, int64_t w_stride) {
+  if (tokens <= 0 || d <= 0 || h <= 0) return 0;
+  const int64_t ldw = stride_of(w_stride, d);
+  Carver cv(nullptr);
+  FfnCopies c;
+  carve_ffn(cv, {tokens, d, h}, Operand{x, tokens, d, stride_of(x_stride, d), 2}, Operand{w_gate, h, d, ldw, 2},
+            Operand{w_up, h, d, ldw, 2}, false, &c);
+  return carved(cv);
+}
+
+msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void* out, void* gate_out, void* up_out,
+                       msign_dtype dtype, msign_activation activation, int64_t tokens, int64_t d, int64_t h,
+                       int64_t x_stride, int64_t w_stride, int64_t out_stride, int64_t pre_stride, void* workspace,
+                       size_t workspace_bytes, msign_stream_t stream_) {
+  const FfnShape s{tokens, d, h};
+  const int act = static_cast<int>(activation);
+  msign_status st = ffn_check(dtype, act, s, x_stride, w_stride);
+  if (st != MSIGN_OK) return st;
+  if (!valid_stride(out_stride, h) || !valid_stride(pre_stride, h)) return MSIGN_ERR_INVALID_ARG;
+  if ((gate_out == nullptr) != (up_out == nullptr)) return MSIGN_ERR_INVALID_ARG;
+  if (tokens == 0 || h == 0) return MSIGN_OK;
+  if (out == nullptr) return MSIGN_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int64_t ldh = stride_of(out_stride, h), ldp = stride_of(pre_stride, h), ldw = stride_of(w_stride, d);
+  void* outs[3] = {out, gate_out, up_out};
+  const int64_t lds[3] = {ldh, ldp, ldp};
+  if (d == 0) {  // both projections are empty sums: gate = up = 0, h = act(0) 0
+    for (int o = 0; o < 3; ++o)
+      if ((st = zero_rows(outs[o], lds[o], tokens, h, 2, stream)) != MSIGN_OK) return st;
+    return MSIGN_OK;
+  }
+  if (x == nullptr || w_gate == nullptr || w_up == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes,
+                    gated_ffn_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))
+    return MSIGN_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  if ((st = layer_state(&dev)) != MSIGN_OK) return st;
+  Operand ox{x, tokens, d, stride_of(x_stride, d), 2}, og{w_gate, h, d, ldw, 2}, ou{w_up, h, d, ldw, 2};
+  {
+    Carver cv(carve_base(workspace));
+    FfnCopies c;
+    carve_ffn(cv, s, ox, og, ou, false, &c);
+    if ((st = place_operand(&ox, c.x, stream)) != MSIGN_OK) return st;
+    if ((st = place_operand(&og, c.wg, stream)) != MSIGN_OK) return st;
+    if ((st = place_operand(&ou, c.wu, stream)) != MSIGN_OK) return st;
+  }
+  const int dt = to_dt(dtype);
+  const CUtensorMapDataType type = tma_type(dt, false);
+  const double flops = 4.0 * tokens * d * h;
+  const double bytes = 2.0 * (static_cast<double>(tokens) * d + 2.0 * h * d + (gate_out ? 3.0 : 1.0) * tokens * h);
+  if (tokens <= kStreamTokens) {
+    StreamParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.bn = static_cast<int>(round_up(tokens, 16));
+    if (!map_rows(&p.tmW[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
+        !map_rows(&p.tmW[1], ou.p, type, 2, h, d, ou.ld, 64, 64) ||
+        !map_rows(&p.tmX, ox.p, type, 2, tokens, d, ox.ld, 64, p.bn))
+      return MSIGN_ERR_CUDA;
+    p.vec_out = 1;
+    for (int o = 0; o < 3; ++o) {
+      p.out[o] = outs[o], p.ldo[o] = lds[o];
+      if (outs[o] != nullptr && (reinterpret_cast<uintptr_t>(outs[o]) % 8 != 0 || (tokens > 1 && lds[o] % 4 != 0)))
+        p.vec_out = 0;
+    }
+    p.tokens = static_cast<int>(tokens), p.N = static_cast<int>(h), p.nk = static_cast<int>(ceil_div(d, 64));
+    p.odt = dt, p.act = act;
+    p.idesc = make_idesc(dt, false, false, false, p.bn, 128);
+    return stream_launch<false, true>(&p, flops, bytes, dev, stream);
+  }
+  PairParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.M = static_cast<int>(tokens), p.N = static_cast<int>(h), p.nk = static_cast<int>(ceil_div(d, 64)), p.segs = 1;
+  if (!map_rows(&p.tmA, ox.p, type, 2, tokens, d, ox.ld, 64, 128) ||
+      !map_rows(&p.tmB[0], og.p, type, 2, h, d, og.ld, 64, 128) ||
+      !map_rows(&p.tmB[1], ou.p, type, 2, h, d, ou.ld, 64, 128) || !pair_outputs(&p, 3, outs, lds, dt))
+    return MSIGN_ERR_CUDA;
+  p.act = act;
+  p.idesc = make_idesc(dt, false, false, false, kBN, kBM);
+  return pair_launch<PAIR_GATED>(&p, 1, flops, bytes, dev, stream);
+}
+
+size_t gated_ffn_backward_workspace_size(int64_t tokens, int64_t d, int64_t h, const void* x, int64_t x_stride,
+                                         const void* w_gate, const void* w_up, int64_t w_stride) {
+  if (tokens <= 0 || d <= 0 || h <= 0) return 0;
+  const int64_t ldw = stride_of(w_stride, d);
+  Carver cv(nullptr);
+  FfnCopies c;
+  carve_ffn(cv, {tokens, d, h}, Operand{x, tokens, d, stride_of(x_stride, d), 2}, Operand{w_gate, h, d, ldw, 2},
+            Operand{w_up, h, d, ldw, 2}, true, &c);
+  return carved(cv);
+}
+
+msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gate, const void* w_up, const void* gate,
+                                const void* up, void* dx, void* dw_gate, void* dw_up, msign_dtype dtype,
+                                msign_dtype grad_dtype, msign_activation activation, int64_t tokens, int64_t d,
+                                int64_t h, int64_t dh_stride, int64_t x_stride, int64_t w_stride, int64_t pre_stride,
+                                int64_t dx_stride, int64_t dw_stride, void* workspace, size_t workspace_bytes,
+                                msign_stream_t stream_) {
+  const FfnShape s{tokens, d, h};
+  const int act = static_cast<int>(activation);
+  msign_status st = ffn_check(dtype, act, s, x_stride, w_stride);
+  if (st != MSIGN_OK) return st;
+  if (!valid_dtype(grad_dtype) || !valid_stride(dh_stride, h) || !valid_stride(pre_stride, h) ||
+      !valid_stride(dx_stride, d) || !valid_stride(dw_stride, d))
+    return MSIGN_ERR_INVALID_ARG;
+  if (grad_dtype != dtype && grad_dtype != MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
+  if ((dw_gate == nullptr) != (dw_up == nullptr) || (dx == nullptr && dw_gate == nullptr))
+    return MSIGN_ERR_INVALID_ARG;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int dt = to_dt(dtype), gdt = to_dt(grad_dtype);
+  const int64_t ldw = stride_of(w_stride, d), ldx = stride_of(x_stride, d), ldh = stride_of(dh_stride, h);
+  const int64_t lddx = stride_of(dx_stride, d), lddw = stride_of(dw_stride, d), ldpre = stride_of(pre_stride, h);
+  if (d == 0) return MSIGN_OK;
+  if (tokens == 0 || h == 0) {  // empty sums
+    if ((st = zero_rows(dx, lddx, tokens, d, 2, stream)) != MSIGN_OK) return st;
+    if ((st = zero_rows(dw_gate, lddw, h, d, dtype_size(gdt), stream)) != MSIGN_OK) return st;
+    return zero_rows(dw_up, lddw, h, d, dtype_size(gdt), stream);
+  }
+  if (dh == nullptr || x == nullptr || w_gate == nullptr || w_up == nullptr || gate == nullptr || up == nullptr)
+    return MSIGN_ERR_INVALID_ARG;
+  if (!workspace_ok(workspace, workspace_bytes,
+                    gated_ffn_backward_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))
+    return MSIGN_ERR_WORKSPACE;
+  DeviceState* dev = nullptr;
+  if ((st = layer_state(&dev)) != MSIGN_OK) return st;
+  Operand ox{x, tokens, d, ldx, 2}, og{w_gate, h, d, ldw, 2}, ou{w_up, h, d, ldw, 2};
+  Carver cv(carve_base(workspace));
+  FfnCopies c;
+  carve_ffn(cv, s, ox, og, ou, true, &c);
+  if (dw_gate != nullptr && (st = place_operand(&ox, c.x, stream)) != MSIGN_OK) return st;
+  if (dx != nullptr && (st = place_operand(&og, c.wg, stream)) != MSIGN_OK) return st;
+  if (dx != nullptr && (st = place_operand(&ou, c.wu, stream)) != MSIGN_OK) return st;
+  st = dt == DT_BF16 ? dact_run<__nv_bfloat16>(dh, ldh, gate, up, ldpre, c.dgu, s, act, stream)
+                     : dact_run<__half>(dh, ldh, gate, up, ldpre, c.dgu, s, act, stream);
+  if (st != MSIGN_OK) return st;
+  const CUtensorMapDataType type = tma_type(dt, false);
+  const int64_t hp = round_up(h, 8);
+  const double flops = 4.0 * tokens * d * h;
+  if (dx != nullptr) {
+    PairParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(tokens), p.N = static_cast<int>(d), p.nk = static_cast<int>(ceil_div(h, 64)), p.segs = 2;
+    void* outs[1] = {dx};
+    if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 128, 2, tokens * hp) ||
+        !map_rows(&p.tmB[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
+        !map_rows(&p.tmB[1], ou.p, type, 2, h, d, ou.ld, 64, 64) || !pair_outputs(&p, 1, outs, &lddx, dt))
+      return MSIGN_ERR_CUDA;
+    p.idesc = make_idesc(dt, false, false, true, kBN, kBM);
+    const double bytes = 2.0 * (2.0 * tokens * h + 2.0 * h * d + static_cast<double>(tokens) * d);
+    if ((st = pair_launch<PAIR_DX>(&p, 1, flops, bytes, dev, stream)) != MSIGN_OK) return st;
+  }
+  if (dw_gate != nullptr) {
+    PairParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = static_cast<int>(h), p.N = static_cast<int>(d), p.nk = static_cast<int>(ceil_div(tokens, 64)), p.segs = 1;
+    void* outs[2] = {dw_gate, dw_up};
+    const int64_t lds[2] = {lddw, lddw};
+    if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 64, 2, tokens * hp) ||
+        !map_rows(&p.tmB[0], ox.p, type, 2, tokens, d, ox.ld, 64, 64) || !pair_outputs(&p, 2, outs, lds, gdt))
+      return MSIGN_ERR_CUDA;
+    p.tmB[1] = p.tmB[0];
+    p.idesc = make_idesc(dt, false, true, true, kBN, kBM);
+    const double bytes = 2.0 * (2.0 * tokens * h + static_cast<double>(tokens) * d) + 2.0 * dtype_size(gdt) * h * d;
+    if ((st = pair_launch<PAIR_DW>(&p, 2, flops, bytes, dev, stream)) != MSIGN_OK) return st;
+  }
+  return MSIGN_OK;
+}
+
+}  // extern "C"

@@ -19,6 +19,7 @@
 #include "msign_b200.h"
 #include "elementwise.cuh"
 #include "gemm_sm100.cuh"
+#include "host_sm100.cuh"
 
 namespace msb {
 
@@ -30,17 +31,8 @@ constexpr int kJordanSteps = 5;
 constexpr float kNsEps = 1e-20f;    // [P2] section 参考实现, under the square root
 constexpr float kGramEps = 1e-7f;   // [P3] Algorithm 2 step 1, added to the norm
 constexpr int kMaxSteps = 64;
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;  // 4 s per wait
 
 // ---------------------------------------------------------------- device state
-
-struct DeviceState {
-  bool ready = false;
-  int sms = 0;
-  int max_pairs = 0;  // CTA pairs of the GEMM kernel that fit on the GPU at once
-  int ingest_blocks = 0;  // ingest_kernel blocks resident at once on the whole GPU
-  int* err = nullptr;
-};
 
 std::mutex g_mu;
 DeviceState g_dev[64];
@@ -152,16 +144,9 @@ void prof_end(int kind, cudaStream_t s, double flops, double bytes) {
 
 // ---------------------------------------------------------------- helpers
 
-inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // NS steps per chained launch: 3 phases each, within kMaxClasses classes.
 constexpr int kChainSteps = 5;
 static_assert(3 * kChainSteps <= kMaxClasses, "a chain of kChainSteps steps fits one launch");
-
-int to_dt(msign_dtype d) { return d == MSIGN_BF16 ? DT_BF16 : d == MSIGN_FP16 ? DT_FP16 : DT_FP32; }
-
-bool valid_dtype(msign_dtype d) { return d == MSIGN_BF16 || d == MSIGN_FP16 || d == MSIGN_FP32; }
 
 // Batch strides: 0 (matrices back to back) or at least one matrix, so that
 // the matrices of a batch never overlap.
@@ -170,19 +155,6 @@ bool valid_strides(int64_t rows, int64_t cols, int64_t in_stride, int64_t out_st
   return in_stride >= 0 && out_stride >= 0 && (in_stride == 0 || in_stride >= per) &&
          (out_stride == 0 || out_stride >= per);
 }
-
-// Workspace carving: the same routine sizes and slices the workspace.
-struct Carver {
-  char* base;
-  size_t off = 0;
-  explicit Carver(void* b) : base(static_cast<char*>(b)) {}
-  void* take(size_t bytes) {
-    off = (off + 1023) & ~size_t(1023);
-    void* p = base ? base + off : nullptr;
-    off += bytes;
-    return p;
-  }
-};
 
 struct Schedule {
   std::vector<float> abc;
@@ -222,19 +194,6 @@ msign_status read_schedule(const msign_coeffs* c, float default_eps, Schedule* s
   }
   s->eps = eps;
   return MSIGN_OK;
-}
-
-// A dense batched matrix: rows x cols, leading dimension ld, batch stride bs
-// (both in elements).
-struct Mat {
-  const void* ptr;
-  int dt;
-  int64_t rows, cols, ld, bs;
-};
-
-bool tma_ok(const Mat& m) {
-  const int es = dtype_size(m.dt);
-  return (reinterpret_cast<uintptr_t>(m.ptr) % 16) == 0 && (m.ld * es) % 16 == 0 && (m.bs * es) % 16 == 0;
 }
 
 // 3-D tensor map (cols, rows, batch) with a box of one 128-byte swizzle row
@@ -541,8 +500,6 @@ msign_status launch_grouped(std::vector<ClassSpec> specs, int ab_dt, cudaStream_
   prof_end(0, stream, flops, bytes);
   return cudaGetLastError() == cudaSuccess ? MSIGN_OK : MSIGN_ERR_CUDA;
 }
-
-msign_status launch_ok() { return cudaGetLastError() == cudaSuccess ? MSIGN_OK : MSIGN_ERR_CUDA; }
 
 // The failure path of every bounded wait, made to fire on purpose: one
 // thread waits on an mbarrier that no one arrives on and on a counter that

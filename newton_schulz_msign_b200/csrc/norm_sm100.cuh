@@ -1,0 +1,526 @@
+// norm_sm100.cuh - root-mean-square norm of rows, with the residual's
+// addition in front, int8 output behind, and its gradients.
+//
+//   z = x + r  (rounded to the io type where r is given: the stored sum)
+//   y_j = z_j w_j / sqrt(mean_j z_j^2 + eps)
+//   int8: scale = max_j |y_j| / 127, q_j = rint(y_j / scale)
+//   dz_j = rstd (dy_j w_j - n_j mean_j(dy_j w_j n_j)) + ds_j,  n = z rstd
+//   dw_j = sum over rows of dy_j n_j
+//
+// All of it is HBM-bound: each row is read once and written once.  A row
+// stays in the registers of the threads that own it (kNormVpt 16-byte pieces
+// each at most), so the statistic, the output and the int8 maximum come from
+// one pass over memory.  Sums and statistics are fp32; y is formed in fp32
+// and rounded once (int8: the fp32 y is quantised, never a rounded one).
+//
+// Rows whose addresses or width do not allow 16-byte accesses, and rows
+// longer than 1024 threads hold, take the *_loop kernels: element by element,
+// the row read again for each pass (it is still in L1 or L2 then).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace msb {
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename T>
+struct Elem {};
+template <>
+struct Elem<float> {
+  static constexpr int vec = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int vec = 8;
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Elem<__half> {
+  static constexpr int vec = 8;
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormBwdThreads = 512;  // the gradients' kernel holds up to 128 registers a thread
+constexpr int kNormVpt = 4;  // 16-byte pieces of a row that one thread holds at most
+
+struct NormArgs {
+  const void *x, *r, *w;  // r, w: may be null
+  void *y, *s;            // y: io type, or int8 (scale set); s: the sum, may be null
+  float* scale;           // int8 output: one a row
+  long long xs, rs, ys, ss;  // row strides in elements
+  long long rows;
+  int cols;
+  int w_f32;  // the weight is fp32 (else the io type)
+  float eps;
+};
+
+struct NormBwdArgs {
+  const void *dy, *z, *w, *ds;  // w, ds: may be null
+  void* dz;
+  float* part;  // [gridDim.x][cols] partial sums of dw, or null
+  float* rstd;  // loop form: [rows]
+  long long dys, zs, dss, dzs;
+  long long rows;
+  int cols;
+  int w_f32;
+  float eps;
+};
+
+// Sums of a and b over the threads of a row: one warp (blockDim.x = 32) or
+// the whole block.  `red` holds 2 x 32 float2; `par` alternates between rows
+// so that one barrier a row is enough (a warp writes a buffer again only
+// after the barrier of the row in between).
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2* red, int par) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  }
+  const int nw = blockDim.x >> 5;
+  if (nw > 1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    red += par * 32;
+    if (lane == 0) red[warp] = make_float2(a, b);
+    __syncthreads();
+    const float2 f = lane < nw ? red[lane] : make_float2(0.0f, 0.0f);
+    a = f.x, b = f.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+  }
+  return make_float2(a, b);
+}
+
+// Largest |v| of a row, given as its bits: as whole numbers they order like
+// the magnitudes, with infinity and then NaN on top, so that a NaN is kept.
+__device__ __forceinline__ uint32_t row_max_bits(uint32_t m, uint32_t* red) {
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  const int nw = blockDim.x >> 5;
+  if (nw > 1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? red[lane] : 0u);
+  }
+  return m;
+}
+
+// The scale of an int8 row and the factor that takes y to q.  A row of zeros
+// has scale 0 and q = 0; one that holds an infinity or a NaN has that as its
+// scale and q = 0, so that what it stands for is NaN throughout.
+__device__ __forceinline__ float q8_factor(uint32_t amax_bits, float* scale) {
+  const float amax = __uint_as_float(amax_bits);
+  *scale = __fdiv_rn(amax, 127.0f);
+  return amax > 0.0f && amax_bits < 0x7F800000u ? __fdiv_rn(127.0f, amax) : 0.0f;
+}
+
+__device__ __forceinline__ int q8(float y, float f) {
+  const int q = __float2int_rn(y * f);  // NaN gives 0
+  return max(-127, min(127, q));
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, int w_f32, int c, float (&v)[Elem<T>::vec]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < Elem<T>::vec; ++i) v[i] = 1.0f;
+  } else if (sizeof(T) == 4 || !w_f32) {
+    Elem<T>::unpack(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + c), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < Elem<T>::vec / 4; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + 4 * i);
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+    }
+  }
+}
+
+// One row per blockDim.x threads (32: a warp a row, blockDim.y rows a block;
+// more: one row a block).  Piece i of thread t starts at column
+// (i blockDim.x + t) vec.
+template <typename T, int VPT, bool Q8>
+__global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArgs a) {
+  constexpr int V = Elem<T>::vec;
+  __shared__ float2 red[64];
+  __shared__ uint32_t redm[32];
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;  // (blocks of several rows have no barrier)
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  uint4 raw[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * V;
+    raw[i] = c < a.cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+  }
+  if (a.r != nullptr) {
+    const T* r = static_cast<const T*>(a.r) + row * a.rs;
+    T* s = static_cast<T*>(a.s) + row * a.ss;
+    uint4 rr[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      rr[i] = c < a.cols ? *reinterpret_cast<const uint4*>(r + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      float xv[V], rv[V];
+      Elem<T>::unpack(raw[i], xv);
+      Elem<T>::unpack(rr[i], rv);
+#pragma unroll
+      for (int j = 0; j < V; ++j) xv[j] += rv[j];
+      raw[i] = Elem<T>::pack(xv);  // the stored sum: what the norm and its gradient see
+      if (c < a.cols && a.s != nullptr) *reinterpret_cast<uint4*>(s + c) = raw[i];
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float v[V];
+    Elem<T>::unpack(raw[i], v);
+#pragma unroll
+    for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
+  }
+  ss = row_sum2(ss, 0.0f, red, 0).x;
+  const float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  if (!Q8) {
+    T* y = static_cast<T*>(a.y) + row * a.ys;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < a.cols) {
+        float v[V], w[V];
+        Elem<T>::unpack(raw[i], v);
+        load_weight<T>(a.w, a.w_f32, c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = v[j] * rstd * w[j];
+        *reinterpret_cast<uint4*>(y + c) = Elem<T>::pack(v);
+      }
+    }
+  } else {
+    int8_t* y = static_cast<int8_t*>(a.y) + row * a.ys;
+    float v[VPT][V];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      Elem<T>::unpack(raw[i], v[i]);
+      if (c < a.cols) {
+        float w[V];
+        load_weight<T>(a.w, a.w_f32, c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          v[i][j] = v[i][j] * rstd * w[j];
+          m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+        }
+      }
+    }
+    float scale;
+    const float f = q8_factor(row_max_bits(m, redm), &scale);
+    if (threadIdx.x == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < a.cols) {
+        uint32_t p[V / 4];
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+          p[j] = (q8(v[i][4 * j], f) & 255) | (q8(v[i][4 * j + 1], f) & 255) << 8 |
+                 (q8(v[i][4 * j + 2], f) & 255) << 16 | (q8(v[i][4 * j + 3], f) & 255) << 24;
+        if (V == 8)
+          *reinterpret_cast<uint2*>(y + c) = make_uint2(p[0], p[V / 4 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(y + c) = p[0];
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const void* w, int w_f32, int c) {
+  if (w == nullptr) return 1.0f;
+  return w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::get(static_cast<const T*>(w)[c]);
+}
+
+// Any width and alignment: one row a block of 256 threads.  A thread reads
+// back only what it wrote itself, so the sum may replace x or r in place.
+template <typename T, bool Q8>
+__global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
+  __shared__ float2 red[64];
+  __shared__ uint32_t redm[32];
+  pdl_wait();
+  pdl_trigger();
+  const long long row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  const T* r = a.r == nullptr ? nullptr : static_cast<const T*>(a.r) + row * a.rs;
+  T* s = a.s == nullptr ? nullptr : static_cast<T*>(a.s) + row * a.ss;
+  // the row's element c as the norm sees it
+  const auto z_at = [&](int c) {
+    float z = Elem<T>::get(x[c]);
+    if (r != nullptr) z = Elem<T>::get(Elem<T>::put(z + Elem<T>::get(r[c])));
+    return z;
+  };
+  float ss = 0.0f;
+  for (int c = threadIdx.x; c < a.cols; c += 256) {
+    const float z = z_at(c);
+    if (s != nullptr) s[c] = Elem<T>::put(z);
+    ss = fmaf(z, z, ss);
+  }
+  if (s != nullptr) x = s, r = nullptr;
+  ss = row_sum2(ss, 0.0f, red, 0).x;
+  const float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  if (!Q8) {
+    T* y = static_cast<T*>(a.y) + row * a.ys;
+    for (int c = threadIdx.x; c < a.cols; c += 256)
+      y[c] = Elem<T>::put(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c));
+  } else {
+    int8_t* y = static_cast<int8_t*>(a.y) + row * a.ys;
+    uint32_t m = 0;
+    for (int c = threadIdx.x; c < a.cols; c += 256)
+      m = max(m, __float_as_uint(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c)) & 0x7FFFFFFFu);
+    float scale;
+    const float f = q8_factor(row_max_bits(m, redm), &scale);
+    if (threadIdx.x == 0) a.scale[row] = scale;
+    for (int c = threadIdx.x; c < a.cols; c += 256)
+      y[c] = static_cast<int8_t>(q8(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c), f));
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+
+// Persistent: block b takes rows b blockDim.y + threadIdx.y, then every
+// gridDim.x blockDim.y further.  The next row's pieces are loaded before the
+// current row's sums are joined, and each thread keeps its columns' share of
+// dw in registers to the end: one partial row of dw a block, joined in a
+// fixed order by dw_reduce_kernel (no atomics: the result does not depend on
+// the order of blocks).
+template <typename T, int VPT>
+__global__ void __launch_bounds__(kNormBwdThreads) rms_norm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int V = Elem<T>::vec;
+  extern __shared__ float sdw[];  // blockDim.y > 1: [blockDim.y][cols]
+  __shared__ float2 red[64];
+  pdl_wait();
+  pdl_trigger();
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
+  const T* z = static_cast<const T*>(a.z);
+  const T* dy = static_cast<const T*>(a.dy);
+  const T* ds = static_cast<const T*>(a.ds);
+  float dw[VPT][V];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < V; ++j) dw[i][j] = 0.0f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 nz[VPT], ny[VPT], ns[VPT];
+  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * V;
+    const bool in = c < a.cols && row < a.rows;
+    nz[i] = in ? *reinterpret_cast<const uint4*>(z + row * a.zs + c) : zero;
+    ny[i] = in ? *reinterpret_cast<const uint4*>(dy + row * a.dys + c) : zero;
+    ns[i] = in && ds != nullptr ? *reinterpret_cast<const uint4*>(ds + row * a.dss + c) : zero;
+  }
+  for (int par = 0; row < a.rows; row += step, par ^= 1) {
+    uint4 rz[VPT], ry[VPT], rs[VPT];
+    float ss = 0.0f, dot = 0.0f;
+    const long long next = row + step;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      rz[i] = nz[i], ry[i] = ny[i], rs[i] = ns[i];
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const bool in = c < a.cols && next < a.rows;
+      nz[i] = in ? *reinterpret_cast<const uint4*>(z + next * a.zs + c) : zero;
+      ny[i] = in ? *reinterpret_cast<const uint4*>(dy + next * a.dys + c) : zero;
+      ns[i] = in && ds != nullptr ? *reinterpret_cast<const uint4*>(ds + next * a.dss + c) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < a.cols) {
+        float zv[V], gv[V], w[V];
+        Elem<T>::unpack(rz[i], zv);
+        Elem<T>::unpack(ry[i], gv);
+        load_weight<T>(a.w, a.w_f32, c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          ss = fmaf(zv[j], zv[j], ss);
+          dot = fmaf(gv[j] * w[j], zv[j], dot);
+        }
+      }
+    }
+    const float2 t = row_sum2(ss, dot, red, par);
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
+    const float m = t.y * rstd * inv;  // mean of dy w n
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < a.cols) {
+        float zv[V], gv[V], w[V], sv[V];
+        Elem<T>::unpack(rz[i], zv);
+        Elem<T>::unpack(ry[i], gv);
+        Elem<T>::unpack(rs[i], sv);
+        load_weight<T>(a.w, a.w_f32, c, w);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float n = zv[j] * rstd;
+          dw[i][j] = fmaf(gv[j], n, dw[i][j]);
+          sv[j] = fmaf(rstd, fmaf(-n, m, gv[j] * w[j]), sv[j]);
+        }
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + row * a.dzs + c) = Elem<T>::pack(sv);
+      }
+    }
+  }
+  if (a.part == nullptr) return;
+  float* out = a.part + static_cast<long long>(blockIdx.x) * a.cols;
+  if (blockDim.y == 1) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = (i * blockDim.x + threadIdx.x) * V;
+      if (c < a.cols)
+#pragma unroll
+        for (int j = 0; j < V; j += 4)
+          *reinterpret_cast<float4*>(out + c + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * V;
+    if (c < a.cols)
+#pragma unroll
+      for (int j = 0; j < V; ++j) sdw[threadIdx.y * a.cols + c + j] = dw[i][j];
+  }
+  __syncthreads();
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.cols; c += blockDim.x * blockDim.y) {
+    float v = 0.0f;
+    for (int y = 0; y < blockDim.y; ++y) v += sdw[y * a.cols + c];
+    out[c] = v;
+  }
+}
+
+// Any width and alignment: dz and the row statistic, one row a block.
+template <typename T>
+__global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArgs a) {
+  __shared__ float2 red[64];
+  pdl_wait();
+  pdl_trigger();
+  const long long row = blockIdx.x;
+  const T* z = static_cast<const T*>(a.z) + row * a.zs;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
+  float ss = 0.0f, dot = 0.0f;
+  for (int c = threadIdx.x; c < a.cols; c += 256) {
+    const float zv = Elem<T>::get(z[c]);
+    ss = fmaf(zv, zv, ss);
+    dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c), zv, dot);
+  }
+  const float2 t = row_sum2(ss, dot, red, 0);
+  const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
+  const float m = t.y * rstd / static_cast<float>(a.cols);
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+  T* dz = static_cast<T*>(a.dz) + row * a.dzs;
+  const T* ds = a.ds == nullptr ? nullptr : static_cast<const T*>(a.ds) + row * a.dss;
+  for (int c = threadIdx.x; c < a.cols; c += 256) {
+    const float n = Elem<T>::get(z[c]) * rstd;
+    const float g = Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c);
+    const float d = rstd * fmaf(-n, m, g);
+    dz[c] = Elem<T>::put(ds != nullptr ? d + Elem<T>::get(ds[c]) : d);
+  }
+}
+
+// Partial sums of dw over the rows of one chunk: thread = column, block row
+// y = chunk.  Reads what the loop form's rows kernel left in rstd.
+template <typename T>
+__global__ void __launch_bounds__(128) rms_norm_dw_loop_kernel(const NormBwdArgs a, int chunk) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 128 + threadIdx.x;
+  if (c >= a.cols) return;
+  const long long r0 = static_cast<long long>(blockIdx.y) * chunk;
+  const long long r1 = min(r0 + chunk, a.rows);
+  float v = 0.0f;
+#pragma unroll 4
+  for (long long r = r0; r < r1; ++r)
+    v = fmaf(Elem<T>::get(static_cast<const T*>(a.dy)[r * a.dys + c]),
+             Elem<T>::get(static_cast<const T*>(a.z)[r * a.zs + c]) * a.rstd[r], v);
+  a.part[static_cast<long long>(blockIdx.y) * a.cols + c] = v;
+}
+
+// dw[c] = sum of part[0..parts)[c], in a fixed order: 32 columns a block, 32
+// threads a column take every 32nd partial, joined in shared memory.
+__global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* part, int parts, int cols, void* dw, int dt) {
+  __shared__ float sh[32][33];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float v = 0.0f;
+  if (c < cols)
+#pragma unroll 4
+    for (int p = threadIdx.y; p < parts; p += 32) v += part[static_cast<long long>(p) * cols + c];
+  sh[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  v = sh[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const int oc = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && oc < cols) store_elem(static_cast<char*>(dw) + static_cast<long long>(oc) * dtype_size(dt), dt, v);
+}
+
+}  // namespace msb
