@@ -32,18 +32,27 @@ def library_path() -> str:
     return _lib.LIB_PATH
 
 
-def _torch():
-    import torch
+_torch_module = None
+_dtype_codes = {}
 
-    return torch
+
+def _torch():
+    """torch, imported on first use."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _dtype_codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
-    if t.dtype not in m:
+    _torch()
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 def _compute_code(name) -> int:
@@ -437,17 +446,18 @@ def _rows_layout(t, name, cols=None):
     form, e.g. ``big[:, :n]``); stride 0 means back to back."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} needs at least one dim")
-    width = t.shape[-1]
+    width = shape[-1]
     if cols is not None and width != cols:
         raise ValueError(f"{name} must have {cols} columns, has {width}")
-    rows = math.prod(t.shape[:-1])
-    if rows * width == 0:
+    rows = math.prod(shape[:-1])
+    if rows * width == 0 or t.is_contiguous():
         return rows, width, 0
     if width > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: each row (the last dim) must be dense")
-    lead = [(t.shape[d], t.stride(d)) for d in range(t.dim() - 1) if t.shape[d] != 1]
+    lead = [(shape[d], t.stride(d)) for d in range(len(shape) - 1) if shape[d] != 1]
     if not lead:
         return rows, width, 0
     for (sz_o, st_o), (sz_i, st_i) in zip(lead[:-1], lead[1:]):
@@ -459,45 +469,88 @@ def _rows_layout(t, name, cols=None):
     return rows, width, (0 if stride == width else stride)
 
 
+def _on(t, index, name):
+    """t lies on the device that the call runs on."""
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
+
+
 def _like(t, ref, name, shape=None, dtype=None):
-    """The given output, checked, or a new one: like ``ref`` but for shape and dtype."""
-    torch = _torch()
-    shape = tuple(ref.shape) if shape is None else tuple(shape)
-    dtype = ref.dtype if dtype is None else dtype
+    """The given output, checked, or a new one: like ``ref`` but for shape and
+    dtype; and its row stride."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    _same_device(t, ref.device, name)
-    if tuple(t.shape) != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {shape} of {dtype}")
-    return t
+        torch = _torch()
+        if shape is not None:
+            return ref.new_empty(shape, dtype=dtype or ref.dtype), 0
+        if not ref.is_contiguous():
+            return torch.empty(ref.shape, dtype=dtype or ref.dtype, device=ref.device), 0
+        return (torch.empty_like(ref) if dtype is None else torch.empty_like(ref, dtype=dtype)), 0
+    shape = ref.shape if shape is None else shape
+    dtype = ref.dtype if dtype is None else dtype
+    _on(t, ref.get_device(), name)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} of {dtype}")
+    return t, _rows_layout(t, name)[2]
 
 
-def _norm_weight(weight, x):
-    """(dtype code, pointer) of a norm's weight."""
+def _call(fn, t, stream, *args):
+    """The status of an entry point called on t's device, with the stream
+    (default: that device's current stream) as its last argument."""
     torch = _torch()
+    index = t.get_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    if torch.cuda.current_device() == index:
+        return fn(*args, stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream)
+
+
+def _call_with_workspace(fn, size_fn, size_args, t, workspace, stream, *args):
+    """_call with a workspace (pointer and bytes) behind args.  Operands that
+    need none, the usual case, are called without asking; the entry point
+    refuses before it enqueues anything where they do."""
+    ws = workspace
+    if ws is not None:
+        _on(ws, t.get_device(), "workspace")
+        return _call(fn, t, stream, *args, ws.data_ptr(), ws.numel() * ws.element_size())
+    st = _call(fn, t, stream, *args, None, 0)
+    if st == _lib.ERR_WORKSPACE:
+        ws, wsb = _workspace(size_fn(*size_args), t.device, None)
+        st = _call(fn, t, stream, *args, ws.data_ptr(), wsb)
+    return st
+
+
+def _norm_weight(weight, x, index):
+    """(dtype code, pointer) of a norm's weight."""
     if weight is None:
-        return _dtype_code(x), None
-    _need_cuda(weight, "weight")
-    _same_device(weight, x.device, "weight")
-    if tuple(weight.shape) != (x.shape[-1],):
+        return _dtype_codes[x.dtype], None
+    _on(weight, index, "weight")
+    if weight.dim() != 1 or weight.shape[0] != x.shape[-1]:
         raise ValueError(f"weight must have shape ({x.shape[-1]},)")
-    if weight.dtype not in (x.dtype, torch.float32):
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    if weight.dtype != x.dtype and weight.dtype != _torch().float32:
         raise TypeError("weight must be of the input's dtype or float32")
-    return _dtype_code(weight), weight.data_ptr()
+    return _dtype_codes[weight.dtype], weight.data_ptr()
 
 
-def _norm_inputs(x, residual, sum_out):
+def _norm_inputs(x, residual, sum_out, index):
+    """(rows, cols, x stride, residual stride, sum, its stride)"""
     rows, cols, xs = _rows_layout(x, "x")
     if residual is None:
         if sum_out is not None:
             raise ValueError("sum_out needs a residual")
         return rows, cols, xs, 0, None, 0
-    _same_device(residual, x.device, "residual")
+    _on(residual, index, "residual")
     if residual.shape != x.shape or residual.dtype != x.dtype:
         raise ValueError("residual must match x in shape and dtype")
-    rs = _rows_layout(residual, "residual")[2]
-    sum_out = _like(sum_out, x, "sum_out")
-    return rows, cols, xs, rs, sum_out, _rows_layout(sum_out, "sum_out")[2]
+    rs = 0 if residual.is_contiguous() else _rows_layout(residual, "residual")[2]
+    return (rows, cols, xs, rs) + _like(sum_out, x, "sum_out")
 
 
 def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_out=None, stream=None):
@@ -507,15 +560,12 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_
     s = x + residual (rounded to x's dtype) when there is a residual.
     ``weight``: of x's dtype or float32, None for ones.  ``sum_out`` may be
     ``x`` or ``residual`` itself, and so may ``out`` where ``sum_out`` is not."""
-    code = _dtype_code(x)
-    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out)
-    wdt, wp = _norm_weight(weight, x)
-    y = _like(out, x, "out")
-    ys = _rows_layout(y, "out")[2]
-    with _torch().cuda.device(x.device):
-        st = _lib.lib().rms_norm(x.data_ptr(), _ptr(residual), wp, y.data_ptr(), _ptr(s), code, wdt, rows, cols, xs, rs,
-                                 ys, ss, float(eps), _stream(stream, x.device))
-    check(st, "rms_norm")
+    code, index = _dtype_code(x), x.get_device()
+    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out, index)
+    wdt, wp = _norm_weight(weight, x, index)
+    y, ys = _like(out, x, "out")
+    check(_call(_lib.lib().rms_norm, x, stream, x.data_ptr(), _ptr(residual), wp, y.data_ptr(), _ptr(s), code, wdt, rows,
+                cols, xs, rs, ys, ss, eps), "rms_norm")
     return y if residual is None else (y, s)
 
 
@@ -524,17 +574,15 @@ def rms_norm_q8(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, s
     """``rms_norm`` with y quantised to int8, one float32 scale a row (max|y| / 127): returns
     (q, scale), or (q, scale, s) when there is a residual.  q * scale[..., None] is what it stands for."""
     torch = _torch()
-    code = _dtype_code(x)
-    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out)
-    wdt, wp = _norm_weight(weight, x)
-    q = _like(out, x, "out", dtype=torch.int8)
-    qs = _rows_layout(q, "out")[2]
-    scale = _like(scale_out, x, "scale_out", shape=x.shape[:-1], dtype=torch.float32)
-    _need_cuda(scale, "scale_out")
-    with torch.cuda.device(x.device):
-        st = _lib.lib().rms_norm_q8(x.data_ptr(), _ptr(residual), wp, q.data_ptr(), scale.data_ptr(), _ptr(s), code, wdt,
-                                    rows, cols, xs, rs, qs, ss, float(eps), _stream(stream, x.device))
-    check(st, "rms_norm_q8")
+    code, index = _dtype_code(x), x.get_device()
+    rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out, index)
+    wdt, wp = _norm_weight(weight, x, index)
+    q, qs = _like(out, x, "out", dtype=torch.int8)
+    scale, _ = _like(scale_out, x, "scale_out", shape=x.shape[:-1], dtype=torch.float32)
+    if scale_out is not None:
+        _need_cuda(scale, "scale_out")
+    check(_call(_lib.lib().rms_norm_q8, x, stream, x.data_ptr(), _ptr(residual), wp, q.data_ptr(), scale.data_ptr(),
+                _ptr(s), code, wdt, rows, cols, xs, rs, qs, ss, eps), "rms_norm_q8")
     return (q, scale) if residual is None else (q, scale, s)
 
 
@@ -548,30 +596,28 @@ def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_ou
 
     ``dsum``: the gradient that reaches s past the norm, added to dx.  dx is
     the gradient of x and of the residual alike; dw is None without a weight."""
-    code = _dtype_code(s)
+    code, index = _dtype_code(s), s.get_device()
     rows, cols, zs = _rows_layout(s, "s")
     strides = []
     for t, nm in ((dy, "dy"), (dsum, "dsum")):
         if t is not None:
-            _same_device(t, s.device, nm)
+            _on(t, index, nm)
             if t.shape != s.shape or t.dtype != s.dtype:
                 raise ValueError(f"{nm} must match s in shape and dtype")
-        strides.append(0 if t is None else _rows_layout(t, nm)[2])
-    wdt, wp = _norm_weight(weight, s)
-    dx = _like(dx_out, s, "dx_out")
-    dxs = _rows_layout(dx, "dx_out")[2]
-    dw = None
+        strides.append(0 if t is None or t.is_contiguous() else _rows_layout(t, nm)[2])
+    wdt, wp = _norm_weight(weight, s, index)
+    dx, dxs = _like(dx_out, s, "dx_out")
+    L = _lib.lib()
+    dw, ws, wsb = None, None, 0
     if weight is not None:
-        dw = _like(dw_out, weight, "dw_out")
-        _need_cuda(dw, "dw_out")
+        dw, _ = _like(dw_out, weight, "dw_out")
+        if dw_out is not None:
+            _need_cuda(dw, "dw_out")
+        ws, wsb = _workspace(L.rms_norm_backward_workspace_size(rows, cols), s.device, workspace)
     elif dw_out is not None:
         raise ValueError("dw_out needs a weight")
-    with _torch().cuda.device(s.device):
-        ws, wsb = _workspace(0 if dw is None else rms_norm_backward_workspace_size(rows, cols), s.device, workspace)
-        st = _lib.lib().rms_norm_backward(dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
-                                          wdt, rows, cols, strides[0], zs, strides[1], dxs, float(eps), _ptr(ws), wsb,
-                                          _stream(stream, s.device))
-    check(st, "rms_norm_backward")
+    check(_call(L.rms_norm_backward, s, stream, dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
+                wdt, rows, cols, strides[0], zs, strides[1], dxs, eps, _ptr(ws), wsb), "rms_norm_backward")
     return dx, dw
 
 
@@ -589,28 +635,26 @@ def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=Non
     float32, or that of ``out``.  ``a`` and ``a_scale`` are what
     ``rms_norm_q8`` returns."""
     torch = _torch()
-    for t, nm in ((a, "a"), (b, "b")):
-        if t.dtype != torch.int8:
-            raise TypeError(f"{nm} must be int8")
+    if a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise TypeError("a and b must be int8")
     if b.dim() != 2:
         raise ValueError("b must be (n, k)")
+    index = a.get_device()
     m, k, sa = _rows_layout(a, "a")
     n, _, sb = _rows_layout(b, "b", k)
-    for t, nm, shape in ((a_scale, "a_scale", tuple(a.shape[:-1])), (b_scale, "b_scale", (n,))):
-        _need_cuda(t, nm)
-        _same_device(t, a.device, nm)
-        if t.dtype != torch.float32 or tuple(t.shape) != shape:
-            raise ValueError(f"{nm} must be float32 of shape {shape}")
-    _same_device(b, a.device, "b")
+    _on(b, index, "b")
+    for t, nm, shape in ((a_scale, "a_scale", a.shape[:-1]), (b_scale, "b_scale", b.shape[:1])):
+        _on(t, index, nm)
+        if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{nm} must be contiguous float32 of shape {tuple(shape)}")
     if out_dtype is None:
         out_dtype = torch.bfloat16 if out is None else out.dtype
-    out = _like(out, a, "out", shape=tuple(a.shape[:-1]) + (n,), dtype=out_dtype)
-    code, so = _dtype_code(out), _rows_layout(out, "out")[2]
-    with torch.cuda.device(a.device):
-        ws, wsb = _workspace(i8_matmul_workspace_size(a, b), a.device, workspace)
-        st = _lib.lib().i8_matmul(a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
-                                  code, m, n, k, sa, sb, so, _ptr(ws), wsb, _stream(stream, a.device))
-    check(st, "i8_matmul")
+    out, so = _like(out, a, "out", shape=a.shape[:-1] + (n,), dtype=out_dtype)
+    code, L = _dtype_code(out), _lib.lib()
+    pa, pb = a.data_ptr(), b.data_ptr()
+    check(_call_with_workspace(L.i8_matmul, L.i8_matmul_workspace_size, (m, n, k, pa, sa, pb, sb), a, workspace, stream, pa,
+                               a_scale.data_ptr(), pb, b_scale.data_ptr(), out.data_ptr(), code, m, n, k, sa, sb, so),
+          "i8_matmul")
     return out
 
 
@@ -628,16 +672,16 @@ def _ffn_inputs(x, w_gate, w_up):
     t, d, xs = _rows_layout(x, "x")
     if w_gate.dim() != 2 or w_gate.shape != w_up.shape:
         raise ValueError("w_gate and w_up must be (h, d) of one shape")
-    strides = []
-    for w, nm in ((w_gate, "w_gate"), (w_up, "w_up")):
-        _same_device(w, x.device, nm)
-        if w.dtype != x.dtype:
-            raise TypeError(f"{nm} must be of x's dtype")
-        h, _, st = _rows_layout(w, nm, d)
-        strides.append(st or d)
-    if strides[0] != strides[1]:
+    if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
+        raise TypeError("w_gate and w_up must be of x's dtype")
+    index = x.get_device()
+    _on(w_gate, index, "w_gate")
+    _on(w_up, index, "w_up")
+    h, _, sg = _rows_layout(w_gate, "w_gate", d)
+    su = _rows_layout(w_up, "w_up")[2]
+    if h > 1 and (sg or d) != (su or d):
         raise ValueError("w_gate and w_up must have one row stride")
-    return t, d, h, xs, strides[0]
+    return t, d, h, xs, sg
 
 
 def gated_ffn_workspace_size(x, w_gate, w_up) -> int:
@@ -653,21 +697,24 @@ def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, 
     ``gate_out`` and ``up_out``) returns (out, gate, up), what
     ``gated_ffn_backward`` takes; else out."""
     code, act = _dtype_code(x), _activation_code(activation)
-    t, d, h, xs, ws_ = _ffn_inputs(x, w_gate, w_up)
-    shape = tuple(x.shape[:-1]) + (h,)
+    t, d, h, xs, sw = _ffn_inputs(x, w_gate, w_up)
+    shape = x.shape[:-1] + (h,)
     if (gate_out is None) != (up_out is None):
         raise ValueError("gate_out and up_out go together")
-    save = save or gate_out is not None
-    out = _like(out, x, "out", shape=shape)
-    gate = _like(gate_out, x, "gate_out", shape=shape) if save else None
-    up = _like(up_out, x, "up_out", shape=shape) if save else None
-    so = _rows_layout(out, "out")[2]
-    sp = _one_stride(gate, "gate_out", up, "up_out", h) if save else 0
-    with _torch().cuda.device(x.device):
-        ws, wsb = _workspace(gated_ffn_workspace_size(x, w_gate, w_up), x.device, workspace)
-        st = _lib.lib().gated_ffn(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), _ptr(gate), _ptr(up),
-                                  code, act, t, d, h, xs, ws_, so, sp, _ptr(ws), wsb, _stream(stream, x.device))
-    check(st, "gated_ffn")
+    out, so = _like(out, x, "out", shape=shape)
+    gate = up = None
+    sp = 0
+    if save or gate_out is not None:
+        save = True
+        gate, sp = _like(gate_out, x, "gate_out", shape=shape)
+        up, su = _like(up_out, x, "up_out", shape=shape)
+        if (sp or h) != (su or h):
+            raise ValueError("gate_out and up_out must have one row stride")
+    L = _lib.lib()
+    px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    check(_call_with_workspace(L.gated_ffn, L.gated_ffn_workspace_size, (t, d, h, px, xs, pg, pu, sw), x, workspace, stream,
+                               px, pg, pu, out.data_ptr(), _ptr(gate), _ptr(up), code, act, t, d, h, xs, sw, so, sp),
+          "gated_ffn")
     return (out, gate, up) if save else out
 
 
@@ -694,33 +741,35 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu
     ``need_dx`` / ``need_dw`` False leaves that part out (None in its place)."""
     torch = _torch()
     code, act = _dtype_code(x), _activation_code(activation)
-    t, d, h, xs, ws_ = _ffn_inputs(x, w_gate, w_up)
+    t, d, h, xs, sw = _ffn_inputs(x, w_gate, w_up)
     if not need_dx and not need_dw:
         raise ValueError("at least one of need_dx and need_dw")
-    shape = tuple(x.shape[:-1]) + (h,)
+    shape, index = x.shape[:-1] + (h,), x.get_device()
     for g, nm in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        _same_device(g, x.device, nm)
-        if tuple(g.shape) != shape or g.dtype != x.dtype:
-            raise ValueError(f"{nm} must be {shape} of x's dtype")
+        _on(g, index, nm)
+        if g.shape != shape or g.dtype != x.dtype:
+            raise ValueError(f"{nm} must be {tuple(shape)} of x's dtype")
     sdh = _rows_layout(dh, "dh")[2]
     sp = _one_stride(gate, "gate", up, "up", h)
     if grad_dtype is None:
         grad_dtype = x.dtype if dw_gate_out is None else dw_gate_out.dtype
     if grad_dtype not in (x.dtype, torch.float32):
         raise TypeError("grad_dtype must be x's dtype or float32")
-    dx = _like(dx_out, x, "dx_out") if need_dx else None
-    dwg = _like(dw_gate_out, w_gate, "dw_gate_out", dtype=grad_dtype) if need_dw else None
-    dwu = _like(dw_up_out, w_up, "dw_up_out", dtype=grad_dtype) if need_dw else None
-    sdx = _rows_layout(dx, "dx_out")[2] if need_dx else 0
-    sdw = _one_stride(dwg, "dw_gate_out", dwu, "dw_up_out", d) if need_dw else 0
-    gcode = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}[grad_dtype]
-    with torch.cuda.device(x.device):
-        ws, wsb = _workspace(gated_ffn_backward_workspace_size(x, w_gate, w_up), x.device, workspace)
-        st = _lib.lib().gated_ffn_backward(dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-                                           gate.data_ptr(), up.data_ptr(), _ptr(dx), _ptr(dwg), _ptr(dwu), code, gcode,
-                                           act, t, d, h, sdh, xs, ws_, sp, sdx, sdw, _ptr(ws), wsb,
-                                           _stream(stream, x.device))
-    check(st, "gated_ffn_backward")
+    dx = dwg = dwu = None
+    sdx = sdw = 0
+    if need_dx:
+        dx, sdx = _like(dx_out, x, "dx_out")
+    if need_dw:
+        dwg, sdw = _like(dw_gate_out, w_gate, "dw_gate_out", dtype=grad_dtype)
+        dwu, su = _like(dw_up_out, w_up, "dw_up_out", dtype=grad_dtype)
+        if (sdw or d) != (su or d):
+            raise ValueError("dw_gate_out and dw_up_out must have one row stride")
+    L = _lib.lib()
+    px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    ws, wsb = _workspace(L.gated_ffn_backward_workspace_size(t, d, h, px, xs, pg, pu, sw), x.device, workspace)
+    check(_call(L.gated_ffn_backward, x, stream, dh.data_ptr(), px, pg, pu, gate.data_ptr(), up.data_ptr(), _ptr(dx),
+                _ptr(dwg), _ptr(dwu), code, _dtype_codes[grad_dtype], act, t, d, h, sdh, xs, sw, sp, sdx, sdw, _ptr(ws),
+                wsb), "gated_ffn_backward")
     return dx, dwg, dwu
 
 

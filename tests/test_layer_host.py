@@ -144,6 +144,9 @@ def test_row_layouts(make, want):
         def stride(self, d):
             return self.t.stride(d)
 
+        def is_contiguous(self):
+            return self.t.is_contiguous()
+
     t = OnDevice(make())
     if want is None:
         with pytest.raises(ValueError):
