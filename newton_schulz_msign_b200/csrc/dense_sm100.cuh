@@ -7,11 +7,12 @@
 //                        accumulator tile a pair (tcgen05.mma.cta_group::2),
 //                        two tiles in TMEM so that one is stored while the
 //                        next is formed, a ring of TMA-fed operand stages.
-//   dense_stream_kernel  few rows (a decoding step).  The weights are the
-//                        M operand and stream through once; the tokens are
-//                        the N operand, as narrow as they are.  A cluster of
-//                        CTAs splits K and joins its parts through
-//                        distributed shared memory.
+//   dense_stream_kernel  few rows (a decoding step), and whatever has too
+//                        few 256 x 256 tiles to fill the GPU.  The weights
+//                        are the M operand and stream through once; the
+//                        tokens are the N operand, as narrow as they are.  A
+//                        cluster of CTAs splits K and joins its parts
+//                        through distributed shared memory.
 //
 // A stage holds 128 bytes of K for every operand row whatever the type (64
 // 16-bit elements or 128 int8), so the 16-bit and the int8 forms share the
@@ -126,7 +127,7 @@ __device__ __forceinline__ float2 act_grad(float g, int act) {
 
 // ---------------------------------------------------------------- many rows
 
-// What a launch of the pair kernel forms:
+// What a launch forms (the layout notes are the pair kernel's):
 //   PAIR_GATED  h = act(x Wg^T) (x Wu^T): the 256 accumulator columns of a
 //               tile are 128 hidden units' gate columns, then the same
 //               units' up columns.  In cta_group::2 each CTA stages half of
@@ -492,18 +493,25 @@ constexpr int kPairSmemBytes =
 
 // ---------------------------------------------------------------- few rows
 
-// out^T = W x^T: 128 weight rows a CTA are the M operand (gated: 64 hidden
-// units' gate rows, then the same units' up rows), bn tokens the N operand.
-// gridDim.x = splits * weight tiles, a cluster being the splits of one tile;
-// gridDim.y = token tiles.
+// out^T = W x^T: 128 output columns a CTA are the M operand (PAIR_GATED: 64
+// hidden units' gate rows, then the same units' up rows), bn output rows
+// ("tokens") the N operand, so that a single token costs an MMA of N = 16.
+//   PAIR_GATED, PAIR_I8  both operands K-major, as they lie
+//   PAIR_DX              M operand Wg, then Wu, MN-major; N operand dg, du
+//   PAIR_DW              M operand x, N operand dg or du (blockIdx.z), both
+//                        MN-major; the "tokens" are the hidden units
+// gridDim.x = splits * column tiles, a cluster being the splits of one tile;
+// gridDim.y = row tiles.
 struct StreamParams {
-  CUtensorMap tmW[2];  // (k, row), box 128 bytes x 128 (gated: x 64, of Wg and Wu)
-  CUtensorMap tmX;     // (k, token), box 128 bytes x bn
-  void* out[3];        // gated: h, gate, up (the last two may be null)
+  CUtensorMap tmW[2];  // K-major: (k, col), box 128 bytes x 128 (gated: x 64, of Wg and Wu); MN-major: (col, k), box 64 x 64
+  CUtensorMap tmX;     // K-major: (k, row, seg), box 128 bytes x bn; MN-major: (row, k, z), box 64 x 64
+  void* out[3];        // PAIR_GATED: h, gate, up (the last two may be null); PAIR_DW: dWg, dWu
   long long ldo[3];
-  const float *sx, *sw;  // int8: a scale a token and a weight row
+  const float *sx, *sw;  // int8: a scale an output row and column
   int tokens, N;         // rows and columns of the output
-  int nk, splits, bn, stages, tmem_cols;
+  int nk, segs;          // K stages a segment, segments
+  int splits, bn, stages, tmem_cols;
+  int push, join_off;    // the splits' sums are pushed, into memory of their own behind the barriers (else pulled)
   int odt, vec_out;      // vec_out: four output columns can be stored at once
   int act;
   uint32_t idesc;
@@ -515,9 +523,12 @@ constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warp
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamATile = 128 * kRowBytes;
 __host__ __device__ inline int stream_stage_bytes(int bn) { return kStreamATile + bn * kRowBytes; }
-__host__ __device__ inline int stream_smem_bytes(int bn, int stages) {
-  return 1024 + stages * stream_stage_bytes(bn) + (2 * kStreamMaxStages + 1) * 8 + 16;
-}
+// Behind the stages: the barriers, then (from the next 1024 bytes on) the join's own memory where it has some.
+__host__ __device__ inline int stream_join_off(int bn, int stages) { return stages * stream_stage_bytes(bn) + 1024; }
+static_assert((2 * kStreamMaxStages + 1) * 8 + 16 <= 1024, "the barriers fit");
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
   float4 v;
@@ -526,6 +537,10 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void store4(void* base, long long at, int dt, bool vec, int n, const float (&v)[4]) {
@@ -552,8 +567,12 @@ __device__ __forceinline__ void store4(void* base, long long at, int dt, bool ve
   for (int i = 0; i < 4 && i < n; ++i) store_elem(p + i * dtype_size(dt), dt, v[i]);
 }
 
-template <bool I8, bool GATED>
-__global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __grid_constant__ StreamParams p) {
+template <int MODE>
+__global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const __grid_constant__ StreamParams p) {
+  constexpr bool I8 = MODE == PAIR_I8;
+  constexpr bool GATED = MODE == PAIR_GATED;
+  constexpr bool kAmn = MODE == PAIR_DX || MODE == PAIR_DW;
+  constexpr bool kBmn = MODE == PAIR_DW;
   constexpr int kBke = I8 ? 128 : 64;
   constexpr int kUnits = GATED ? 64 : 128;  // output columns a tile
   extern __shared__ uint8_t smem_raw[];
@@ -568,13 +587,14 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int split = static_cast<int>(cluster_ctarank());
-  const int tile = blockIdx.x / p.splits;
-  const int unit0 = tile * kUnits;
-  const int tok0 = blockIdx.y * p.bn;
+  const int unit0 = static_cast<int>(blockIdx.x) / p.splits * kUnits;
+  const int tok0 = static_cast<int>(blockIdx.y) * p.bn;
+  const int z = MODE == PAIR_DW ? static_cast<int>(blockIdx.z) : 0;
   const uint64_t limit = p.timeout_ns;
   // this CTA's K stages
-  const int kbeg = static_cast<int>(static_cast<long long>(p.nk) * split / p.splits);
-  const int kend = static_cast<int>(static_cast<long long>(p.nk) * (split + 1) / p.splits);
+  const int steps = p.nk * p.segs;
+  const int kbeg = static_cast<int>(static_cast<long long>(steps) * split / p.splits);
+  const int kend = static_cast<int>(static_cast<long long>(steps) * (split + 1) / p.splits);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -589,14 +609,15 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
     tmem_alloc(s_tmem, p.tmem_cols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 2 && lane == 0) {
     tma_prefetch_desc(&p.tmW[0]);
-    if (GATED) tma_prefetch_desc(&p.tmW[1]);
+    if (GATED || MODE == PAIR_DX) tma_prefetch_desc(&p.tmW[1]);
     tma_prefetch_desc(&p.tmX);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.push) cluster_arrive();
   const uint32_t tmem_base = *s_tmem;
   pdl_wait();
   pdl_trigger();
@@ -604,18 +625,25 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0, used = 0, last_phase = 0;
-    for (int kb = kbeg; kb < kend; ++kb) {
+    for (int step = kbeg; step < kend; ++step) {
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(&empty[stage], phase ^ 1u, s_abort, p.err, limit))) break;
       uint8_t* dst = smem + stage * stage_bytes;
+      uint8_t* dstx = dst + kStreamATile;
       mbar_arrive_expect_tx_w(&full[stage], static_cast<uint32_t>(stage_bytes));
-      const int k0 = kb * kBke;
-      if (GATED) {
-        tma_load_3d_w(dst, &p.tmW[0], &full[stage], k0, unit0, 0);
-        tma_load_3d_w(dst + kStreamATile / 2, &p.tmW[1], &full[stage], k0, unit0, 0);
+      const int seg = MODE == PAIR_DX && step >= p.nk ? 1 : 0;
+      const int k0 = (step - seg * p.nk) * kBke;
+      if (kAmn) {
+        tma_load_3d_w(dst, &p.tmW[seg], &full[stage], unit0, k0, 0);
+        tma_load_3d_w(dst + kStreamATile / 2, &p.tmW[seg], &full[stage], unit0 + 64, k0, 0);
       } else {
         tma_load_3d_w(dst, &p.tmW[0], &full[stage], k0, unit0, 0);
+        if (GATED) tma_load_3d_w(dst + kStreamATile / 2, &p.tmW[1], &full[stage], k0, unit0, 0);
       }
-      tma_load_3d_w(dst + kStreamATile, &p.tmX, &full[stage], k0, tok0, 0);
+      if (kBmn) {
+        for (int c = 0; c < p.bn; c += 64) tma_load_3d_w(dstx + c * kRowBytes, &p.tmX, &full[stage], tok0 + c, k0, z);
+      } else {
+        tma_load_3d_w(dstx, &p.tmX, &full[stage], k0, tok0, seg);
+      }
       used |= 1u << stage;
       last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
       if (++stage == p.stages) {
@@ -630,19 +658,21 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
   } else if (warp == 1) {
     int stage = 0;
     uint32_t phase = 0;
-    const uint64_t d0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-    for (int kb = kbeg; kb < kend; ++kb) {
+    const uint32_t s0 = smem_u32(smem), x0 = s0 + kStreamATile;
+    const uint64_t dA = kAmn ? smem_desc_sw128(s0, 8192, 1024) : smem_desc_sw128(s0, 16, 1024);
+    const uint64_t dB = kBmn ? smem_desc_sw128(x0, 8192, 1024) : smem_desc_sw128(x0, 16, 1024);
+    constexpr uint32_t ka = kAmn ? 2048 >> 4 : 32 >> 4, kb = kBmn ? 2048 >> 4 : 32 >> 4;
+    for (int step = kbeg; step < kend; ++step) {
       if (!__all_sync(0xFFFFFFFFu, wait_bounded(&full[stage], phase, s_abort, p.err, limit))) break;
       tc_fence_after();
-      const uint64_t da = d0 + static_cast<uint64_t>((stage * stage_bytes) >> 4);
-      const uint64_t db = da + static_cast<uint64_t>(kStreamATile >> 4);
+      const uint64_t at = static_cast<uint64_t>((stage * stage_bytes) >> 4);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t acc = (kb > kbeg || kk > 0) ? 1u : 0u;
+        const uint32_t acc = (step > kbeg || kk > 0) ? 1u : 0u;
         if (I8)
-          umma_i8_w(tmem_base, da + 2 * kk, db + 2 * kk, p.idesc, acc);
+          umma_i8_w(tmem_base, dA + at + kk * ka, dB + at + kk * kb, p.idesc, acc);
         else
-          umma_f16_w(tmem_base, da + 2 * kk, db + 2 * kk, p.idesc, acc);
+          umma_f16_w(tmem_base, dA + at + kk * ka, dB + at + kk * kb, p.idesc, acc);
       }
       umma_commit_w(&empty[stage]);
       if (++stage == p.stages) {
@@ -655,52 +685,81 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
     tc_fence_before();
   }
   __syncwarp();
-  __syncthreads();  // the MMAs are done and no copy is in flight: the stages hold the partial sums from here on
-  float* part = reinterpret_cast<float*>(smem);  // [bn tokens][128 weight rows]
+  __syncthreads();  // the MMAs are done and no copy is in flight
+  // Join the splits: each rank of the cluster owns `chunk` of the tile's
+  // rows.  Few rows (push): every rank writes its sums of a row to the owner
+  // through distributed shared memory, which waits for nothing.  More (pull):
+  // each rank keeps its sums where its stages were, and the owner reads them
+  // 16 bytes at a time -- single remote words cost more than the round trip
+  // from about 32 rows on (77 x 4096 x 14336 int8: 17.7 us pushed, 15.7
+  // pulled; 1 x 4096 x 4096: 4.9 and 5.5).
   const int toks = min(p.bn, p.tokens - tok0);
+  const int chunk = (toks + p.splits - 1) / p.splits;
+  const bool push = p.push != 0;
+  float* part = reinterpret_cast<float*>(smem + (push ? p.join_off : 0));  // push: [rank][chunk][128]; pull: [row][128]
+  if (push) cluster_wait();  // every rank has started
   if (warp >= 2) {
     tc_fence_after();
     const int q = warp & 3;
     const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const int col = q * 32 + lane;
+    const uint32_t mine = smem_u32(part + split * chunk * 128 + col);
+    int owner = 0, local = 0;  // of the row being written
     for (int c = 0; c < toks; c += 16) {
       uint32_t raw[16];
       tmem_ld_32x32b_x16(acc0 + c, raw);
       tmem_wait_ld();
+      if (!push) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        part[(c + i) * 128 + q * 32 + lane] = __uint_as_float(raw[i]);  // int8: the int32 bits
+        for (int i = 0; i < 16; ++i) part[(c + i) * 128 + col] = __uint_as_float(raw[i]);  // int8: the int32 bits
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i < toks) st_dsmem(mapa_shared(mine, owner) + static_cast<uint32_t>(local) * 512u, raw[i]);
+          if (++local == chunk) local = 0, ++owner;
+        }
+      }
     }
     tc_fence_before();
   }
   __syncwarp();
-  cluster_sync_all();
-  // Join the splits in their order (int8: whole numbers) and store: four
-  // consecutive units of one token a thread, a token's units side by side.
+  if (p.splits > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
+  // Sum the ranks' parts in their order (int8: whole numbers) and store: four
+  // consecutive columns of one row a thread, a row's columns side by side.
   constexpr int kQuads = kUnits / 4;
-  const uint32_t part0 = smem_u32(part);
-  const int items = toks * kQuads;
-  for (int i = split * kStreamThreads + threadIdx.x; i < items; i += p.splits * kStreamThreads) {
-    const int tok = i / kQuads, c = (i - tok * kQuads) * 4;
+  const int items = max(0, min(chunk, toks - split * chunk)) * kQuads;
+  for (int i = threadIdx.x; i < items; i += kStreamThreads) {
+    const int local = i / kQuads, c = (i - local * kQuads) * 4;
     if (unit0 + c >= p.N) continue;
-    const uint32_t at = part0 + static_cast<uint32_t>(tok * 128 + c) * 4u;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int iv[4] = {0, 0, 0, 0};
-    for (int s = 0; s < p.splits; ++s) {
-      const uint32_t remote = mapa_shared(at, s);
-      const float4 f = ld_dsmem_f4(remote);
+    const auto add = [&](const float4& f, const float4& g) {
       if (I8) {
         iv[0] += __float_as_int(f.x), iv[1] += __float_as_int(f.y);
         iv[2] += __float_as_int(f.z), iv[3] += __float_as_int(f.w);
       } else {
         v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
       }
-      if (GATED) {
-        const float4 g = ld_dsmem_f4(remote + 64 * 4);
-        u[0] += g.x, u[1] += g.y, u[2] += g.z, u[3] += g.w;
+      if (GATED) u[0] += g.x, u[1] += g.y, u[2] += g.z, u[3] += g.w;
+    };
+    if (push || p.splits == 1) {
+      const float4* at = reinterpret_cast<const float4*>(part) + local * 32 + (c >> 2);
+      for (int s = 0; s < p.splits; ++s, at += chunk * 32) add(at[0], GATED ? at[16] : at[0]);
+    } else {
+      const uint32_t at = smem_u32(part + (split * chunk + local) * 128 + c);
+      for (int s = 0; s < p.splits; s += 2) {  // (two or more ranks, a power of two)
+        const uint32_t a0 = mapa_shared(at, s), a1 = mapa_shared(at, s + 1);
+        const float4 f0 = ld_dsmem_f4(a0), f1 = ld_dsmem_f4(a1);
+        const float4 g0 = GATED ? ld_dsmem_f4(a0 + 256) : f0, g1 = GATED ? ld_dsmem_f4(a1 + 256) : f1;
+        add(f0, g0);
+        add(f1, g1);
       }
     }
     const int n = p.N - (unit0 + c);
-    const long long tk = tok0 + tok;
+    const long long tk = tok0 + split * chunk + local;
     if (I8) {
       const float sx = p.sx[tk];
 #pragma unroll
@@ -717,11 +776,11 @@ __global__ void __launch_bounds__(kStreamThreads) dense_stream_kernel(const __gr
         store4(p.out[2], tk * p.ldo[2] + unit0 + c, p.odt, p.vec_out, n, u);
       }
     } else {
-      store4(p.out[0], tk * p.ldo[0] + unit0 + c, p.odt, p.vec_out, n, v);
+      store4(p.out[z], tk * p.ldo[z] + unit0 + c, p.odt, p.vec_out, n, v);
     }
   }
   __syncwarp();
-  cluster_sync_all();  // no CTA leaves while another may read its part
+  if (!push && p.splits > 1) cluster_sync_all();  // no CTA leaves while another may read its part
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -759,39 +818,42 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const U* in, long long ld
 // dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
 // rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
 // io type here, as the operands of the products that follow.
+//
+// 64 threads of a block take eight columns each, its four rows of threads
+// every (4 gridDim.y)-th row.  VEC: the inputs allow 16-byte loads; else they
+// are loaded one by one, and only the stores are wide.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) gated_dact_kernel(const T* dh, long long ldh, const T* gate, long long ldg,
-                                                         const T* up, long long ldu, T* out, long long ldp,
-                                                         long long rows, int cols, int act) {
+__global__ void __launch_bounds__(256) gated_dact_kernel(const T* dh, long long ldh, const T* gate, const T* up,
+                                                         long long ldg, T* out, long long ldp, long long rows,
+                                                         int cols, int act) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = VEC ? Elem<T>::vec : 1;
+  const long long c = (static_cast<long long>(blockIdx.x) * 64 + threadIdx.x) * 8;
+  if (c >= cols) return;
   const long long zs = rows * ldp;
-  const long long per = (cols + V - 1) / V;
-  const long long total = rows * per;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 256ll * gridDim.x) {
-    const long long r = i / per;
-    const int c = static_cast<int>(i - r * per) * V;
-    T* o = out + r * ldp + c;  // dg; du lies zs further
+  for (long long r = static_cast<long long>(blockIdx.y) * 4 + threadIdx.y; r < rows; r += 4ll * gridDim.y) {
+    float d[8], g[8], u[8];
     if (VEC) {
-      float d[Elem<T>::vec], g[Elem<T>::vec], u[Elem<T>::vec];
       Elem<T>::unpack(*reinterpret_cast<const uint4*>(dh + r * ldh + c), d);
       Elem<T>::unpack(*reinterpret_cast<const uint4*>(gate + r * ldg + c), g);
-      Elem<T>::unpack(*reinterpret_cast<const uint4*>(up + r * ldu + c), u);
-#pragma unroll
-      for (int j = 0; j < Elem<T>::vec; ++j) {
-        const float2 a = act_grad(g[j], act);
-        g[j] = d[j] * u[j] * a.y;
-        d[j] = d[j] * a.x;
-      }
-      *reinterpret_cast<uint4*>(o) = Elem<T>::pack(g);
-      *reinterpret_cast<uint4*>(o + zs) = Elem<T>::pack(d);
+      Elem<T>::unpack(*reinterpret_cast<const uint4*>(up + r * ldg + c), u);
     } else {
-      const float d = Elem<T>::get(dh[r * ldh + c]);
-      const float2 a = act_grad(Elem<T>::get(gate[r * ldg + c]), act);
-      o[0] = Elem<T>::put(d * Elem<T>::get(up[r * ldu + c]) * a.y);
-      o[zs] = Elem<T>::put(d * a.x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = c + j < cols;
+        d[j] = in ? Elem<T>::get(dh[r * ldh + c + j]) : 0.0f;
+        g[j] = in ? Elem<T>::get(gate[r * ldg + c + j]) : 0.0f;
+        u[j] = in ? Elem<T>::get(up[r * ldg + c + j]) : 0.0f;
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 a = act_grad(g[j], act);
+      g[j] = d[j] * u[j] * a.y;
+      d[j] = d[j] * a.x;
+    }
+    *reinterpret_cast<uint4*>(out + r * ldp + c) = Elem<T>::pack(g);
+    *reinterpret_cast<uint4*>(out + zs + r * ldp + c) = Elem<T>::pack(d);
   }
 }
 

@@ -150,6 +150,8 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
 // Partial rows of dw that the gradients leave at most: four blocks an SM.
 constexpr int64_t kDwParts = 4 * kPlanSms;
 constexpr int64_t kDwLoopParts = 128;  // row chunks of the loop form
+constexpr int kSmemMax = 232448;       // shared memory of a block
+constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has some static shared memory too)
 
 template <typename T>
 msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char* ws, double bytes,
@@ -157,18 +159,26 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char*
   Carver cv(ws);
   float* part = static_cast<float*>(cv.take(sizeof(float) * std::min<int64_t>(a.rows, kDwParts) * a.cols));
   float* rstd = static_cast<float*>(cv.take(sizeof(float) * a.rows));
-  NormPlan p;
-  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec, 8, 1, kNormBwdThreads, kNormVpt);
   a.part = dw != nullptr ? part : nullptr;
   int64_t parts;
   msign_status st;
-  if (p.vec) {
-    const int threads = static_cast<int>(p.block.x * p.block.y);
-    parts = std::min<int64_t>(ceil_div(a.rows, p.block.y),
-                              int64_t(kPlanSms) * std::max(1, std::min(4, 1024 / threads)));
-    const size_t smem = p.block.y > 1 && dw != nullptr ? sizeof(float) * p.block.y * a.cols : 0;
-    auto* k = p.vpt == 1 ? rms_norm_bwd_kernel<T, 1> : p.vpt == 2 ? rms_norm_bwd_kernel<T, 2> : rms_norm_bwd_kernel<T, 4>;
-    st = launch(k, dim3(static_cast<unsigned>(parts)), p.block, smem, 0, 3, 0.0, bytes, stream, a);
+  const int64_t pieces = a.cols / Elem<T>::vec;
+  const int row_bytes = a.cols * static_cast<int>(sizeof(T));
+  const int arrays = a.ds != nullptr ? 3 : 2;
+  if (vec_ok && pieces <= kNormBwdThreads * kNormBwdVpt) {
+    int vpt = pieces <= 32 ? 1 : 2;
+    while (pieces > vpt * kNormBwdThreads) vpt *= 2;
+    const int x = static_cast<int>(round_up(ceil_div(pieces, vpt), 32));
+    const int y = std::max(1, kNormBwdThreads / x);
+    int per_sm = vpt <= 2 ? 3 : vpt <= 4 ? 2 : 1;  // by the kernel's registers
+    const int slot = arrays * y * row_bytes;
+    int stages = std::min(kNormRing, kNormRingMax / per_sm / slot);
+    while (stages < 2) stages = std::min(kNormRing, kNormRingMax / --per_sm / slot);
+    parts = std::min<int64_t>({ceil_div(a.rows, y), int64_t(kPlanSms) * per_sm, kDwParts});  // what the workspace holds
+    auto* k = vpt == 1 ? rms_norm_bwd_kernel<T, 1> : vpt == 2 ? rms_norm_bwd_kernel<T, 2>
+              : vpt == 4 ? rms_norm_bwd_kernel<T, 4> : rms_norm_bwd_kernel<T, 8>;
+    st = launch(k, dim3(static_cast<unsigned>(parts)), dim3(x, y), static_cast<size_t>(stages) * slot, 0, 3, 0.0,
+                bytes, stream, a, stages);
     if (st != MSIGN_OK) return st;
   } else {
     a.rstd = dw != nullptr ? rstd : nullptr;
@@ -254,26 +264,26 @@ uint32_t make_idesc(int dt, bool i8, bool a_mn, bool b_mn, int n, int m) {
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-template <int MODE>
-msign_status pair_setup() {
-  return cudaFuncSetAttribute(dense_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmemBytes) ==
-                 cudaSuccess
+template <typename K>
+msign_status smem_limit(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
              ? MSIGN_OK
              : MSIGN_ERR_CUDA;
 }
 
-template <bool I8, bool GATED>
-msign_status stream_setup() {
-  return cudaFuncSetAttribute(dense_stream_kernel<I8, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) ==
-                 cudaSuccess
-             ? MSIGN_OK
-             : MSIGN_ERR_CUDA;
+template <typename T>
+msign_status norm_bwd_limits() {
+  msign_status st = smem_limit(rms_norm_bwd_kernel<T, 1>, kNormRingMax);
+  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 2>, kNormRingMax);
+  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 4>, kNormRingMax);
+  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 8>, kNormRingMax);
+  return st;
 }
 
 std::mutex g_layer_mu;
 bool g_layer_ready[64] = {};
 
-// The device's state, with the product kernels' shared memory limits raised.
+// The device's state, with the kernels' shared memory limits raised.
 msign_status layer_state(DeviceState** out) {
   msign_status st = device_state(out);
   if (st != MSIGN_OK) return st;
@@ -281,8 +291,12 @@ msign_status layer_state(DeviceState** out) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSIGN_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_layer_mu);
   if (g_layer_ready[dev]) return MSIGN_OK;
-  for (msign_status s : {pair_setup<PAIR_GATED>(), pair_setup<PAIR_I8>(), pair_setup<PAIR_DX>(), pair_setup<PAIR_DW>(),
-                         stream_setup<true, false>(), stream_setup<false, true>()})
+  for (msign_status s :
+       {smem_limit(dense_pair_kernel<PAIR_GATED>, kPairSmemBytes), smem_limit(dense_pair_kernel<PAIR_I8>, kPairSmemBytes),
+        smem_limit(dense_pair_kernel<PAIR_DX>, kPairSmemBytes), smem_limit(dense_pair_kernel<PAIR_DW>, kPairSmemBytes),
+        smem_limit(dense_stream_kernel<PAIR_GATED>, kSmemMax), smem_limit(dense_stream_kernel<PAIR_I8>, kSmemMax),
+        smem_limit(dense_stream_kernel<PAIR_DX>, kSmemMax), smem_limit(dense_stream_kernel<PAIR_DW>, kSmemMax),
+        norm_bwd_limits<__nv_bfloat16>(), norm_bwd_limits<__half>(), norm_bwd_limits<float>()})
     if (s != MSIGN_OK) return s;
   g_layer_ready[dev] = true;
   return MSIGN_OK;
@@ -322,26 +336,89 @@ msign_status pair_launch(PairParams* p, int64_t nz, double flops, double bytes, 
   return launch(dense_pair_kernel<MODE>, dim3(grid), dim3(kThreads), kPairSmemBytes, 0, 0, flops, bytes, stream, *p);
 }
 
-// Tokens that the stream kernel takes.
-constexpr int64_t kStreamTokens = 256;
+// Whether a product of `rows` x `cols` outputs (`z` of them) goes to the
+// stream kernel: few rows, or too few 256-row tiles to keep the CTA pairs
+// busy.
+template <int MODE>
+bool stream_takes(int64_t rows, int64_t cols, int64_t z) {
+  return rows <= 128 || ceil_div(rows, kBM) * ceil_div(cols, MODE == PAIR_GATED ? 128 : kBN) * z < 48;
+}
 
-template <bool I8, bool GATED>
-msign_status stream_launch(StreamParams* p, double flops, double bytes, DeviceState* dev, cudaStream_t stream) {
-  const int units = GATED ? 64 : 128;
-  const int64_t tiles = ceil_div(p->N, units);
-  if (tiles > INT32_MAX / 16) return MSIGN_ERR_UNSUPPORTED;
+
+// Tile of a stream launch: the N operand's width (output rows a tile), the K
+// splits (the cluster's width) and the shared memory of a CTA.  The least of
+// an estimate in microseconds: the loads (each stage's 128 + bn rows of 128
+// bytes) at 120 KB/us on the busiest SM and 100 on the average one, 0.02 a row
+// of the tile for the join and the store, 1 and a quarter a rank for a join
+// between ranks, and 3 for every further generation of CTAs.  Measured against single choices for
+// all: tiles of at most 128 rows lose 22% on the 400 x 1000 x 2736 gated block
+// (18.7 against 14.5 us), tiles of 256 rows 25% on 256 x 4096 x 4096 int8
+// (15 against 11.8).
+struct StreamPlan {
+  int bn, splits, budget;
+};
+
+template <int MODE>
+StreamPlan stream_plan(int64_t rows, int64_t cols, int64_t z, int64_t steps) {
+  const int64_t unit = MODE == PAIR_DW ? 64 : 16;
+  const int64_t tiles = ceil_div(cols, MODE == PAIR_GATED ? 64 : 128) * z;
+  StreamPlan best = {};
+  double least = 0.0;
+  for (int64_t wide : {256, 192, 160, 128, 96, 64}) {
+    const int64_t bn = round_up(ceil_div(rows, ceil_div(rows, wide)), unit);  // equal tiles
+    const int64_t per_sm = bn <= 128 ? 2 : 1;  // by shared memory
+    for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
+      const int64_t ctas = tiles * ceil_div(rows, bn) * splits;
+      const int64_t gens = ceil_div(ctas, per_sm * kPlanSms);
+      const double kb = ceil_div(steps, splits) * (128 + bn) * 128 / 1e3;  // loads of a CTA
+      const double busiest = static_cast<double>(per_sm == 1 ? gens : ceil_div(ctas, kPlanSms));
+      const double mean = per_sm == 1 ? static_cast<double>(gens) : std::max(1.0, static_cast<double>(ctas) / kPlanSms);
+      const double us = std::max(kb * busiest / 120, kb * mean / 100) + 0.02 * bn +
+                        (splits > 1 ? 1.0 + 0.25 * splits : 0.0) +
+                        3.0 * (gens - 1);
+      if (best.bn == 0 || us < least) {
+        least = us;
+        best = {static_cast<int>(bn), splits, per_sm == 2 ? 113 * 1024 : 220 * 1024};
+      }
+    }
+  }
+  return best;
+}
+
+template <int MODE>
+msign_status stream_launch(StreamParams* p, const StreamPlan& plan, int64_t z, double flops, double bytes,
+                           DeviceState* dev, cudaStream_t stream) {
+  const int64_t tiles = ceil_div(p->N, MODE == PAIR_GATED ? 64 : 128), rows = ceil_div(p->tokens, plan.bn);
+  if (tiles > INT32_MAX / 16 || rows > 65535) return MSIGN_ERR_UNSUPPORTED;
+  p->bn = plan.bn;
+  p->splits = plan.splits;
   p->tmem_cols = 32;
   while (p->tmem_cols < p->bn) p->tmem_cols *= 2;
-  // narrow token tiles: two CTAs an SM
-  const int budget = p->bn <= 64 ? 113 * 1024 : 220 * 1024;
-  p->stages = std::min(kStreamMaxStages, (budget - stream_smem_bytes(p->bn, 0)) / stream_stage_bytes(p->bn));
-  const int64_t slots = p->bn <= 64 ? 2 * kPlanSms : kPlanSms;
-  p->splits = 1;
-  while (p->splits < 8 && tiles * p->splits * 2 <= slots && p->nk >= 8 * p->splits) p->splits *= 2;
+  // what a rank holds of the sums
+  const int join = p->splits * static_cast<int>(ceil_div(std::min(p->bn, p->tokens), p->splits)) * 512;
+  p->push = p->splits > 1 && join <= 32 * 1024;
+  const int fixed = 2048 + (p->push ? join : 0);  // alignment, barriers, the pushed sums
+  p->stages = std::min(kStreamMaxStages, (plan.budget - fixed) / stream_stage_bytes(p->bn));
+  // pulled sums lie where the stages were
+  while (!p->push && p->stages * stream_stage_bytes(p->bn) < p->bn * 512) ++p->stages;
+  p->join_off = stream_join_off(p->bn, p->stages);
   p->err = dev->err;
   p->timeout_ns = kWaitLimitNs;
-  return launch(dense_stream_kernel<I8, GATED>, dim3(static_cast<unsigned>(tiles * p->splits), 1),
-                dim3(kStreamThreads), stream_smem_bytes(p->bn, p->stages), p->splits, 0, flops, bytes, stream, *p);
+  return launch(dense_stream_kernel<MODE>,
+                dim3(static_cast<unsigned>(tiles * p->splits), static_cast<unsigned>(rows), static_cast<unsigned>(z)),
+                dim3(kStreamThreads), p->stages * stream_stage_bytes(p->bn) + fixed, p->splits, 0, flops, bytes, stream, *p);
+}
+
+// Output pointers and row strides of a stream launch.
+void stream_outputs(StreamParams* p, int n, void* const* out, const int64_t* ld, int odt) {
+  const int es = dtype_size(odt);
+  p->odt = odt;
+  p->vec_out = 1;
+  for (int o = 0; o < n; ++o) {
+    p->out[o] = out[o], p->ldo[o] = ld[o];
+    if (out[o] != nullptr && (reinterpret_cast<uintptr_t>(out[o]) % (4 * es) != 0 || (p->tokens > 1 && ld[o] % 4 != 0)))
+      p->vec_out = 0;
+  }
 }
 
 msign_status zero_rows(void* p, int64_t ld, int64_t rows, int64_t cols, int es, cudaStream_t stream) {
@@ -393,11 +470,13 @@ msign_status dact_run(const void* dh, int64_t ldh, const void* gate, const void*
   const int64_t ldp = round_up(s.h, 8);
   const bool vec = s.h % 8 == 0 && rows_aligned(dh, ldh, s.t, 2) && rows_aligned(gate, ldp_in, s.t, 2) &&
                    rows_aligned(up, ldp_in, s.t, 2);
-  const int64_t items = s.t * (vec ? s.h / 8 : s.h);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(items, 256), 16 * kPlanSms)));
+  // about 16 blocks an SM, each a few rows
+  const int64_t gx = ceil_div(ldp, 512);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(
+                                                 ceil_div(s.t, 4), std::max<int64_t>(1, 16 * kPlanSms / gx))));
   auto* k = vec ? gated_dact_kernel<T, true> : gated_dact_kernel<T, false>;
-  return launch(k, grid, dim3(256), 0, 0, 3, 0.0, 10.0 * s.t * s.h, stream, static_cast<const T*>(dh), ldh,
-                static_cast<const T*>(gate), ldp_in, static_cast<const T*>(up), ldp_in, static_cast<T*>(dgu), ldp, s.t,
+  return launch(k, grid, dim3(64, 4), 0, 0, 3, 0.0, 10.0 * s.t * s.h, stream, static_cast<const T*>(dh), ldh,
+                static_cast<const T*>(gate), static_cast<const T*>(up), ldp_in, static_cast<T*>(dgu), ldp, s.t,
                 static_cast<int>(s.h), act);
 }
 
@@ -463,13 +542,14 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   if (dw != nullptr && !workspace_ok(workspace, workspace_bytes, rms_norm_backward_workspace_size(rows, cols)))
     return MSIGN_ERR_WORKSPACE;
   DeviceState* dev = nullptr;
-  msign_status st = device_state(&dev);
+  msign_status st = layer_state(&dev);
   if (st != MSIGN_OK) return st;
   NormBwdArgs a = {};
   a.dy = dy, a.z = sum, a.w = weight, a.ds = dsum, a.dz = dx;
   a.dys = stride_of(dy_stride, cols), a.zs = stride_of(sum_stride, cols);
   a.dss = stride_of(dsum_stride, cols), a.dzs = stride_of(dx_stride, cols);
   a.rows = rows, a.cols = static_cast<int>(cols), a.w_f32 = w_dtype == MSIGN_FP32, a.eps = eps;
+  a.err = dev->err, a.timeout_ns = kWaitLimitNs;
   const bool vec = cols % v == 0 && rows_aligned(dy, a.dys, rows, es) && rows_aligned(sum, a.zs, rows, es) &&
                    rows_aligned(dx, a.dzs, rows, es) && (dsum == nullptr || rows_aligned(dsum, a.dss, rows, es)) &&
                    (weight == nullptr || aligned16(weight));
@@ -523,20 +603,18 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
   const double flops = 2.0 * m * n * k;
   const double bytes = static_cast<double>(m) * k + static_cast<double>(n) * k + static_cast<double>(oes) * m * n;
   const CUtensorMapDataType type = tma_type(0, true);
-  if (m <= kStreamTokens) {
+  if (stream_takes<PAIR_I8>(m, n, 1)) {
     StreamParams p;
     std::memset(&p, 0, sizeof(p));
-    p.bn = static_cast<int>(round_up(m, 16));
+    p.tokens = static_cast<int>(m), p.N = static_cast<int>(n), p.nk = static_cast<int>(ceil_div(k, 128)), p.segs = 1;
+    const StreamPlan plan = stream_plan<PAIR_I8>(m, n, 1, p.nk);
     if (!map_rows(&p.tmW[0], ob.p, type, 1, n, k, ob.ld, 128, 128) ||
-        !map_rows(&p.tmX, oa.p, type, 1, m, k, oa.ld, 128, p.bn))
+        !map_rows(&p.tmX, oa.p, type, 1, m, k, oa.ld, 128, plan.bn))
       return MSIGN_ERR_CUDA;
-    p.out[0] = out, p.ldo[0] = ldo;
+    stream_outputs(&p, 1, &out, &ldo, odt);
     p.sx = a_scale, p.sw = b_scale;
-    p.tokens = static_cast<int>(m), p.N = static_cast<int>(n), p.nk = static_cast<int>(ceil_div(k, 128));
-    p.odt = odt;
-    p.vec_out = reinterpret_cast<uintptr_t>(out) % (4 * oes) == 0 && (m <= 1 || ldo % 4 == 0);
-    p.idesc = make_idesc(0, true, false, false, p.bn, 128);
-    return stream_launch<true, false>(&p, flops, bytes, dev, stream);
+    p.idesc = make_idesc(0, true, false, false, plan.bn, 128);
+    return stream_launch<PAIR_I8>(&p, plan, 1, flops, bytes, dev, stream);
   }
   PairParams p;
   std::memset(&p, 0, sizeof(p));
@@ -605,24 +683,19 @@ msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void
   const CUtensorMapDataType type = tma_type(dt, false);
   const double flops = 4.0 * tokens * d * h;
   const double bytes = 2.0 * (static_cast<double>(tokens) * d + 2.0 * h * d + (gate_out ? 3.0 : 1.0) * tokens * h);
-  if (tokens <= kStreamTokens) {
+  if (stream_takes<PAIR_GATED>(tokens, h, 1)) {
     StreamParams p;
     std::memset(&p, 0, sizeof(p));
-    p.bn = static_cast<int>(round_up(tokens, 16));
+    p.tokens = static_cast<int>(tokens), p.N = static_cast<int>(h), p.nk = static_cast<int>(ceil_div(d, 64)), p.segs = 1;
+    const StreamPlan plan = stream_plan<PAIR_GATED>(tokens, h, 1, p.nk);
     if (!map_rows(&p.tmW[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
         !map_rows(&p.tmW[1], ou.p, type, 2, h, d, ou.ld, 64, 64) ||
-        !map_rows(&p.tmX, ox.p, type, 2, tokens, d, ox.ld, 64, p.bn))
+        !map_rows(&p.tmX, ox.p, type, 2, tokens, d, ox.ld, 64, plan.bn))
       return MSIGN_ERR_CUDA;
-    p.vec_out = 1;
-    for (int o = 0; o < 3; ++o) {
-      p.out[o] = outs[o], p.ldo[o] = lds[o];
-      if (outs[o] != nullptr && (reinterpret_cast<uintptr_t>(outs[o]) % 8 != 0 || (tokens > 1 && lds[o] % 4 != 0)))
-        p.vec_out = 0;
-    }
-    p.tokens = static_cast<int>(tokens), p.N = static_cast<int>(h), p.nk = static_cast<int>(ceil_div(d, 64));
-    p.odt = dt, p.act = act;
-    p.idesc = make_idesc(dt, false, false, false, p.bn, 128);
-    return stream_launch<false, true>(&p, flops, bytes, dev, stream);
+    stream_outputs(&p, 3, outs, lds, dt);
+    p.act = act;
+    p.idesc = make_idesc(dt, false, false, false, plan.bn, 128);
+    return stream_launch<PAIR_GATED>(&p, plan, 1, flops, bytes, dev, stream);
   }
   PairParams p;
   std::memset(&p, 0, sizeof(p));
@@ -694,31 +767,61 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
   const int64_t hp = round_up(h, 8);
   const double flops = 4.0 * tokens * d * h;
   if (dx != nullptr) {
-    PairParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.M = static_cast<int>(tokens), p.N = static_cast<int>(d), p.nk = static_cast<int>(ceil_div(h, 64)), p.segs = 2;
-    void* outs[1] = {dx};
-    if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 128, 2, tokens * hp) ||
-        !map_rows(&p.tmB[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
-        !map_rows(&p.tmB[1], ou.p, type, 2, h, d, ou.ld, 64, 64) || !pair_outputs(&p, 1, outs, &lddx, dt))
-      return MSIGN_ERR_CUDA;
-    p.idesc = make_idesc(dt, false, false, true, kBN, kBM);
     const double bytes = 2.0 * (2.0 * tokens * h + 2.0 * h * d + static_cast<double>(tokens) * d);
-    if ((st = pair_launch<PAIR_DX>(&p, 1, flops, bytes, dev, stream)) != MSIGN_OK) return st;
+    const int nk = static_cast<int>(ceil_div(h, 64));
+    if (stream_takes<PAIR_DX>(tokens, d, 1)) {
+      StreamParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.tokens = static_cast<int>(tokens), p.N = static_cast<int>(d), p.nk = nk, p.segs = 2;
+      const StreamPlan plan = stream_plan<PAIR_DX>(tokens, d, 1, 2 * static_cast<int64_t>(nk));
+      if (!map_rows(&p.tmW[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
+          !map_rows(&p.tmW[1], ou.p, type, 2, h, d, ou.ld, 64, 64) ||
+          !map_rows(&p.tmX, c.dgu, type, 2, tokens, h, hp, 64, plan.bn, 2, tokens * hp))
+        return MSIGN_ERR_CUDA;
+      stream_outputs(&p, 1, &dx, &lddx, dt);
+      p.idesc = make_idesc(dt, false, true, false, plan.bn, 128);
+      st = stream_launch<PAIR_DX>(&p, plan, 1, flops, bytes, dev, stream);
+    } else {
+      PairParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.M = static_cast<int>(tokens), p.N = static_cast<int>(d), p.nk = nk, p.segs = 2;
+      if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 128, 2, tokens * hp) ||
+          !map_rows(&p.tmB[0], og.p, type, 2, h, d, og.ld, 64, 64) ||
+          !map_rows(&p.tmB[1], ou.p, type, 2, h, d, ou.ld, 64, 64) || !pair_outputs(&p, 1, &dx, &lddx, dt))
+        return MSIGN_ERR_CUDA;
+      p.idesc = make_idesc(dt, false, false, true, kBN, kBM);
+      st = pair_launch<PAIR_DX>(&p, 1, flops, bytes, dev, stream);
+    }
+    if (st != MSIGN_OK) return st;
   }
   if (dw_gate != nullptr) {
-    PairParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.M = static_cast<int>(h), p.N = static_cast<int>(d), p.nk = static_cast<int>(ceil_div(tokens, 64)), p.segs = 1;
+    const double bytes = 2.0 * (2.0 * tokens * h + static_cast<double>(tokens) * d) + 2.0 * dtype_size(gdt) * h * d;
+    const int nk = static_cast<int>(ceil_div(tokens, 64));
     void* outs[2] = {dw_gate, dw_up};
     const int64_t lds[2] = {lddw, lddw};
-    if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 64, 2, tokens * hp) ||
-        !map_rows(&p.tmB[0], ox.p, type, 2, tokens, d, ox.ld, 64, 64) || !pair_outputs(&p, 2, outs, lds, gdt))
-      return MSIGN_ERR_CUDA;
-    p.tmB[1] = p.tmB[0];
-    p.idesc = make_idesc(dt, false, true, true, kBN, kBM);
-    const double bytes = 2.0 * (2.0 * tokens * h + static_cast<double>(tokens) * d) + 2.0 * dtype_size(gdt) * h * d;
-    if ((st = pair_launch<PAIR_DW>(&p, 2, flops, bytes, dev, stream)) != MSIGN_OK) return st;
+    if (ceil_div(h, kBM) * ceil_div(d, kBN) * 2 < 48 && nk >= 32) {
+      StreamParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.tokens = static_cast<int>(h), p.N = static_cast<int>(d), p.nk = nk, p.segs = 1;
+      const StreamPlan plan = stream_plan<PAIR_DW>(h, d, 2, nk);
+      if (!map_rows(&p.tmW[0], ox.p, type, 2, tokens, d, ox.ld, 64, 64) ||
+          !map_rows(&p.tmX, c.dgu, type, 2, tokens, h, hp, 64, 64, 2, tokens * hp))
+        return MSIGN_ERR_CUDA;
+      stream_outputs(&p, 2, outs, lds, gdt);
+      p.idesc = make_idesc(dt, false, true, true, plan.bn, 128);
+      st = stream_launch<PAIR_DW>(&p, plan, 2, flops, bytes, dev, stream);
+    } else {
+      PairParams p;
+      std::memset(&p, 0, sizeof(p));
+      p.M = static_cast<int>(h), p.N = static_cast<int>(d), p.nk = nk, p.segs = 1;
+      if (!map_rows(&p.tmA, c.dgu, type, 2, tokens, h, hp, 64, 64, 2, tokens * hp) ||
+          !map_rows(&p.tmB[0], ox.p, type, 2, tokens, d, ox.ld, 64, 64) || !pair_outputs(&p, 2, outs, lds, gdt))
+        return MSIGN_ERR_CUDA;
+      p.tmB[1] = p.tmB[0];
+      p.idesc = make_idesc(dt, false, true, true, kBN, kBM);
+      st = pair_launch<PAIR_DW>(&p, 2, flops, bytes, dev, stream);
+    }
+    if (st != MSIGN_OK) return st;
   }
   return MSIGN_OK;
 }

@@ -24,10 +24,22 @@
 
 #include <cstdint>
 
+#include "gemm_sm100.cuh"
+#include "ptx_sm100.cuh"
+
 namespace msb {
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// `bytes` (a multiple of 16, both addresses too) from global to this CTA's
+// shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 template <typename T>
 struct Elem {};
@@ -91,8 +103,45 @@ struct Elem<__half> {
   }
 };
 
+// Two fp32 values at a time: the gradients' kernel is bound by instructions
+// as soon as its loads are asynchronous.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pair2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float2 unpair2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4& u, f32x2 (&v)[Elem<T>::vec / 2]) {
+  float f[Elem<T>::vec];
+  Elem<T>::unpack(u, f);
+#pragma unroll
+  for (int j = 0; j < Elem<T>::vec / 2; ++j) v[j] = pair2(f[2 * j], f[2 * j + 1]);
+}
+
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBwdThreads = 512;  // the gradients' kernel holds up to 128 registers a thread
+constexpr int kNormBwdThreads = 256;  // largest block of the gradients' kernel
+constexpr int kNormBwdVpt = 8;        // and pieces of a row that one of its threads holds at most
 constexpr int kNormVpt = 4;  // 16-byte pieces of a row that one thread holds at most
 
 struct NormArgs {
@@ -116,6 +165,8 @@ struct NormBwdArgs {
   int cols;
   int w_f32;
   float eps;
+  int* err;  // device error word, and the limit of a wait
+  unsigned long long timeout_ns;
 };
 
 // Sums of a and b over the threads of a row: one warp (blockDim.x = 32) or
@@ -344,114 +395,184 @@ __global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
 
 // ---------------------------------------------------------------- gradients
 
-// Persistent: block b takes rows b blockDim.y + threadIdx.y, then every
-// gridDim.x blockDim.y further.  The next row's pieces are loaded before the
-// current row's sums are joined, and each thread keeps its columns' share of
-// dw in registers to the end: one partial row of dw a block, joined in a
-// fixed order by dw_reduce_kernel (no atomics: the result does not depend on
-// the order of blocks).
+// Persistent: a block takes blockDim.y rows at a time, blockDim.x threads
+// each (whole warps; piece i of thread t starts at column (i blockDim.x + t)
+// vec), block b the row groups b, b + gridDim.x, ...  The rows' dy, z and ds
+// come through a ring of `stages` slots of shared memory filled by bulk
+// copies, so that the loads in flight depend neither on registers nor on the
+// barrier that joins a row's sums.  A slot is filled again after the barrier
+// of the group behind it: every thread has passed its last read of the slot
+// by then.  Each thread keeps its columns' share of dw in registers to the
+// end: one partial row of dw a block, joined in a fixed order by
+// dw_reduce_kernel (no atomics: the result does not depend on the order of
+// blocks).
+constexpr int kNormRing = 8;
+
 template <typename T, int VPT>
-__global__ void __launch_bounds__(kNormBwdThreads) rms_norm_bwd_kernel(const NormBwdArgs a) {
-  constexpr int V = Elem<T>::vec;
-  extern __shared__ float sdw[];  // blockDim.y > 1: [blockDim.y][cols]
-  __shared__ float2 red[64];
+__global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1)
+    rms_norm_bwd_kernel(const NormBwdArgs a, int stages) {
+  constexpr int V = Elem<T>::vec, H = V / 2;
+  extern __shared__ __align__(128) uint8_t ring[];  // [stages][z, dy, ds][blockDim.y][cols]
+  __shared__ float2 red[2][kNormBwdThreads / 32];
+  __shared__ uint64_t full[kNormRing];
+  const int lane = threadIdx.x & 31;
+  const int ny = blockDim.y, nwarp = blockDim.x >> 5;       // rows of a group, warps of a row
+  const int warp0 = threadIdx.y * nwarp;                    // this row's first warp
+  const int warp = warp0 + (threadIdx.x >> 5);
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const int arrays = a.ds != nullptr ? 3 : 2;
+  const uint32_t slot = static_cast<uint32_t>(arrays * ny) * row_bytes;
+  const long long step = static_cast<long long>(gridDim.x) * ny;
+  // the group of rows from `row0` on into slot st, by the first warp: a copy a lane
+  const auto fill = [&](long long row0, int st) {
+    const int n = static_cast<int>(min(static_cast<long long>(ny), a.rows - row0));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(arrays * n) * row_bytes);
+    __syncwarp();
+    for (int i = lane; i < arrays * n; i += 32) {
+      const int arr = i / n, y = i - arr * n;
+      const void* src = arr == 0   ? static_cast<const T*>(a.z) + (row0 + y) * a.zs
+                        : arr == 1 ? static_cast<const T*>(a.dy) + (row0 + y) * a.dys
+                                   : static_cast<const T*>(a.ds) + (row0 + y) * a.dss;
+      bulk_load(ring + st * slot + (arr * ny + y) * row_bytes, src, row_bytes, &full[st]);
+    }
+  };
+  if (threadIdx.x == 0 && threadIdx.y == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.y;
-  const T* z = static_cast<const T*>(a.z);
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* ds = static_cast<const T*>(a.ds);
-  float dw[VPT][V];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < V; ++j) dw[i][j] = 0.0f;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 nz[VPT], ny[VPT], ns[VPT];
-  long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  long long row0 = static_cast<long long>(blockIdx.x) * ny;
+  if (warp == 0)
+    for (int i = 0; i < stages; ++i)
+      if (row0 + i * step < a.rows) fill(row0 + i * step, i);
+  f32x2 dw[VPT][H], w[VPT][H];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * blockDim.x + threadIdx.x) * V;
-    const bool in = c < a.cols && row < a.rows;
-    nz[i] = in ? *reinterpret_cast<const uint4*>(z + row * a.zs + c) : zero;
-    ny[i] = in ? *reinterpret_cast<const uint4*>(dy + row * a.dys + c) : zero;
-    ns[i] = in && ds != nullptr ? *reinterpret_cast<const uint4*>(ds + row * a.dss + c) : zero;
+    float f[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = 0.0f;
+    if (c < a.cols) load_weight<T>(a.w, a.w_f32, c, f);
+#pragma unroll
+    for (int j = 0; j < H; ++j) dw[i][j] = 0, w[i][j] = pair2(f[2 * j], f[2 * j + 1]);
   }
-  for (int par = 0; row < a.rows; row += step, par ^= 1) {
-    uint4 rz[VPT], ry[VPT], rs[VPT];
-    float ss = 0.0f, dot = 0.0f;
-    const long long next = row + step;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      rz[i] = nz[i], ry[i] = ny[i], rs[i] = ns[i];
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      const bool in = c < a.cols && next < a.rows;
-      nz[i] = in ? *reinterpret_cast<const uint4*>(z + next * a.zs + c) : zero;
-      ny[i] = in ? *reinterpret_cast<const uint4*>(dy + next * a.dys + c) : zero;
-      ns[i] = in && ds != nullptr ? *reinterpret_cast<const uint4*>(ds + next * a.dss + c) : zero;
-    }
+  const float inv = 1.0f / static_cast<float>(a.cols);
+  int st = 0, last = -1;
+  uint32_t phase = 0;
+  bool ok = true;
+  for (int par = 0; row0 < a.rows; row0 += step, par ^= 1) {
+    const long long row = row0 + threadIdx.y;
+    const bool mine = row < a.rows;
+    ok = ok && wait_bounded(&full[st], phase, nullptr, a.err, a.timeout_ns);
+    const uint8_t* src = ring + st * slot + threadIdx.y * row_bytes;
+    uint4 rz[VPT], ry[VPT];
+    f32x2 ss2 = 0, dot2 = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c < a.cols) {
-        float zv[V], gv[V], w[V];
-        Elem<T>::unpack(rz[i], zv);
-        Elem<T>::unpack(ry[i], gv);
-        load_weight<T>(a.w, a.w_f32, c, w);
+      if (mine && c < a.cols) {
+        f32x2 zv[H], gv[H];
+        rz[i] = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
+        ry[i] = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
+        unpack2<T>(rz[i], zv);
+        unpack2<T>(ry[i], gv);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          ss = fmaf(zv[j], zv[j], ss);
-          dot = fmaf(gv[j] * w[j], zv[j], dot);
+        for (int j = 0; j < H; ++j) {
+          ss2 = fma2(zv[j], zv[j], ss2);
+          dot2 = fma2(mul2(gv[j], w[i][j]), zv[j], dot2);
         }
       }
     }
-    const float2 t = row_sum2(ss, dot, red, par);
-    const float inv = 1.0f / static_cast<float>(a.cols);
-    const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
-    const float m = t.y * rstd * inv;  // mean of dy w n
+    float ss = unpair2(ss2).x + unpair2(ss2).y, dot = unpair2(dot2).x + unpair2(dot2).y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+    }
+    if (lane == 0) red[par][warp] = make_float2(ss, dot);
+    __syncthreads();
+    // (past the barrier: the slot of the group before is free)
+    if (warp == 0 && last >= 0 && row0 + (stages - 1) * step < a.rows) fill(row0 + (stages - 1) * step, last);
+    if (nwarp > 1) {  // every thread adds the row's warps up, in their order
+      ss = dot = 0.0f;
+      for (int i = 0; i < nwarp; ++i) {
+        const float2 f = red[par][warp0 + i];
+        ss += f.x, dot += f.y;
+      }
+    }
+    const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
+    const float m = -dot * rstd * inv;  // minus the mean of dy w n
+    const f32x2 rstd2 = pair2(rstd, rstd), m2 = pair2(m, m);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c < a.cols) {
-        float zv[V], gv[V], w[V], sv[V];
-        Elem<T>::unpack(rz[i], zv);
-        Elem<T>::unpack(ry[i], gv);
-        Elem<T>::unpack(rs[i], sv);
-        load_weight<T>(a.w, a.w_f32, c, w);
+      if (mine && c < a.cols) {
+        f32x2 zv[H], gv[H], sv[H];
+        unpack2<T>(rz[i], zv);
+        unpack2<T>(ry[i], gv);
+        if (arrays == 3) {
+          unpack2<T>(*reinterpret_cast<const uint4*>(src + 2 * ny * row_bytes + c * sizeof(T)), sv);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float n = zv[j] * rstd;
-          dw[i][j] = fmaf(gv[j], n, dw[i][j]);
-          sv[j] = fmaf(rstd, fmaf(-n, m, gv[j] * w[j]), sv[j]);
+          for (int j = 0; j < H; ++j) sv[j] = 0;
         }
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + row * a.dzs + c) = Elem<T>::pack(sv);
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          const f32x2 n = mul2(zv[j], rstd2);
+          dw[i][j] = fma2(gv[j], n, dw[i][j]);
+          const float2 d = unpair2(fma2(rstd2, fma2(n, m2, mul2(gv[j], w[i][j])), sv[j]));
+          o[2 * j] = d.x, o[2 * j + 1] = d.y;
+        }
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + row * a.dzs + c) = Elem<T>::pack(o);
       }
     }
+    last = st;
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!ok && warp == 0 && lane == 0) {
+    // a wait ran out: no copy may still be landing when the block ends
+    const long long groups = (a.rows - static_cast<long long>(blockIdx.x) * ny + step - 1) / step;
+    for (int i = 0; i < stages && i < groups; ++i)
+      wait_bounded(&full[i], static_cast<uint32_t>((groups - 1 - i) / stages) & 1u, nullptr, a.err, a.timeout_ns);
   }
   if (a.part == nullptr) return;
   float* out = a.part + static_cast<long long>(blockIdx.x) * a.cols;
-  if (blockDim.y == 1) {
+  if (ny == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
       if (c < a.cols)
 #pragma unroll
-        for (int j = 0; j < V; j += 4)
-          *reinterpret_cast<float4*>(out + c + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+        for (int j = 0; j < H; j += 2) {
+          const float2 lo = unpair2(dw[i][j]), hi = unpair2(dw[i][j + 1]);
+          *reinterpret_cast<float4*>(out + c + 2 * j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
     }
     return;
   }
+  // the group's rows first join their shares in the ring, which is free now
+  float* sdw = reinterpret_cast<float*>(ring);  // [blockDim.y][cols]
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * blockDim.x + threadIdx.x) * V;
     if (c < a.cols)
 #pragma unroll
-      for (int j = 0; j < V; ++j) sdw[threadIdx.y * a.cols + c + j] = dw[i][j];
+      for (int j = 0; j < H; j += 2) {
+        const float2 lo = unpair2(dw[i][j]), hi = unpair2(dw[i][j + 1]);
+        *reinterpret_cast<float4*>(sdw + threadIdx.y * a.cols + c + 2 * j) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
   }
   __syncthreads();
-  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.cols; c += blockDim.x * blockDim.y) {
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.cols; c += blockDim.x * ny) {
     float v = 0.0f;
-    for (int y = 0; y < blockDim.y; ++y) v += sdw[y * a.cols + c];
+    for (int y = 0; y < ny; ++y) v += sdw[y * a.cols + c];
     out[c] = v;
   }
 }
