@@ -102,27 +102,69 @@ constexpr float kGeluA = 0.044715f;
 // quotient is 0 there, as it should be.
 __device__ __forceinline__ float g_sigmoid(float g, float v) { return __fdividef(g, 1.0f + __expf(-v)); }
 
-__device__ __forceinline__ float act_of(float g, int act) {
-  if (act == ACT_SILU) return g_sigmoid(g, g);
-  if (act == ACT_GELU) return g * normcdff(g);  // (keeps its relative accuracy in the tail, unlike 1 + erf)
+template <int ACT>
+__device__ __forceinline__ float act_of(float g) {
+  if (ACT == ACT_SILU) return g_sigmoid(g, g);
+  if (ACT == ACT_GELU) return g * (0.5f * erfcf(-0.70710678118654752f * g));  // (1 + erf would lose the tail's digits)
   // (1 + tanh z) / 2 = sigmoid(2 z)
   return g_sigmoid(g, 2.0f * kGeluC * fmaf(kGeluA * g * g, g, g));
 }
 
 // act(g) and act'(g)
-__device__ __forceinline__ float2 act_grad(float g, int act) {
-  if (act == ACT_SILU) {
-    const float p = 1.0f / (1.0f + __expf(-g));
+template <int ACT>
+__device__ __forceinline__ float2 act_grad(float g) {
+  if (ACT == ACT_SILU) {
+    const float p = __fdividef(1.0f, 1.0f + __expf(-g));
     return make_float2(g * p, p * fmaf(g, 1.0f - p, 1.0f));
   }
-  if (act == ACT_GELU) {
-    const float c = normcdff(g);
+  if (ACT == ACT_GELU) {
+    const float c = 0.5f * erfcf(-0.70710678118654752f * g);
     return make_float2(g * c, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), c));
   }
   // past |g| = 30 p is 0 or 1 to the last bit: the clamp only keeps the cube finite
   const float c = fminf(fmaxf(g, -30.0f), 30.0f);
-  const float p = 1.0f / (1.0f + __expf(-2.0f * kGeluC * fmaf(kGeluA * c * c, c, c)));
+  const float p = __fdividef(1.0f, 1.0f + __expf(-2.0f * kGeluC * fmaf(kGeluA * c * c, c, c)));
   return make_float2(g * p, fmaf(2.0f * p * (1.0f - p), kGeluC * fmaf(3.0f * kGeluA * c * c, c, c), p));
+}
+
+// u_i <- act(g_i) u_i.  The choice stands outside the loops: inside, every
+// unrolled element carried all three activations, and the gated epilogue
+// spent its time on fetching code (10100 cycles a tile against 4000).
+template <int ACT, int N>
+__device__ __forceinline__ void gate_mul_as(const float (&g)[N], float (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] *= act_of<ACT>(g[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void gate_mul(const float (&g)[N], float (&u)[N], int act) {
+  if (act == ACT_SILU)
+    gate_mul_as<ACT_SILU>(g, u);
+  else if (act == ACT_GELU)
+    gate_mul_as<ACT_GELU>(g, u);
+  else
+    gate_mul_as<ACT_GELU_TANH>(g, u);
+}
+
+// From d = dh, g and u: g <- dh u act'(g), d <- dh act(g).
+template <int ACT, int N>
+__device__ __forceinline__ void gate_grad_as(float (&d)[N], float (&g)[N], const float (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 a = act_grad<ACT>(g[i]);
+    g[i] = d[i] * u[i] * a.y;
+    d[i] = d[i] * a.x;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void gate_grad(float (&d)[N], float (&g)[N], const float (&u)[N], int act) {
+  if (act == ACT_SILU)
+    gate_grad_as<ACT_SILU>(d, g, u);
+  else if (act == ACT_GELU)
+    gate_grad_as<ACT_GELU>(d, g, u);
+  else
+    gate_grad_as<ACT_GELU_TANH>(d, g, u);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -408,8 +450,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const PairTile tc = pair_tile(p, t);
       const int row0 = tc.tm * kBM + static_cast<int>(rank) * kHalfM + q * 32;
       const int col0 = tc.tn * kCols + half * (kCols / 2);
-      float sa = 0.0f;
-      if (kI8 && row0 + lane < p.M) sa = p.sa[row0 + lane];
+      // int8: this lane's row scale, and its columns' scales of the warp's four blocks
+      float sa = 0.0f, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (kI8) {
+        if (row0 + lane < p.M) sa = p.sa[row0 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col0 + 32 * j + lane < p.N) sb[j] = p.sb[col0 + 32 * j + lane];
+      }
       int ok = 1;
       if (lane == 0) ok = wait_bounded(&tfull[buf], bphase, s_abort, p.err, limit) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -427,8 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float g[32], u[32];
             tmem_block(acc0 + j * 32, g);
             tmem_block(acc0 + 128 + j * 32, u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] *= act_of(g[i], p.act);
+            gate_mul(g, u, p.act);
             box_put16(box, lane, j, u, p.odt);
           }
           box_send(p, 0, box, lane, row0, col0);
@@ -454,12 +501,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tmem_block(acc0 + (j + i2) * 32, v);
               if (kI8) {
                 // the int32 sum is exact; one rounding to fp32, one for each scale
-                const int c = col0 + (j + i2) * 32;
+                const int b = j + i2;
+                const float s = b == 0 ? sb[0] : b == 1 ? sb[1] : b == 2 ? sb[2] : sb[3];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float sb = c + i < p.N ? __ldg(p.sb + c + i) : 0.0f;
-                  v[i] = static_cast<float>(__float_as_int(v[i])) * sa * sb;
-                }
+                for (int i = 0; i < 32; ++i)
+                  v[i] = static_cast<float>(__float_as_int(v[i])) * sa * __shfl_sync(0xFFFFFFFFu, s, i);
               }
               if (p.odt == DT_FP32)
                 box_put32(box, lane, v);
@@ -767,9 +813,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
         v[j] = j < n ? static_cast<float>(iv[j]) * sx * p.sw[unit0 + c + j] : 0.0f;
     }
     if (GATED) {
-      float h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = act_of(v[j], p.act) * u[j];
+      float h[4] = {u[0], u[1], u[2], u[3]};
+      gate_mul(v, h, p.act);
       store4(p.out[0], tk * p.ldo[0] + unit0 + c, p.odt, p.vec_out, n, h);
       if (p.out[1] != nullptr) {
         store4(p.out[1], tk * p.ldo[1] + unit0 + c, p.odt, p.vec_out, n, v);
@@ -846,12 +891,7 @@ __global__ void __launch_bounds__(256) gated_dact_kernel(const T* dh, long long 
         u[j] = in ? Elem<T>::get(up[r * ldg + c + j]) : 0.0f;
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 a = act_grad(g[j], act);
-      g[j] = d[j] * u[j] * a.y;
-      d[j] = d[j] * a.x;
-    }
+    gate_grad(d, g, u, act);
     *reinterpret_cast<uint4*>(out + r * ldp + c) = Elem<T>::pack(g);
     *reinterpret_cast<uint4*>(out + zs + r * ldp + c) = Elem<T>::pack(d);
   }

@@ -632,9 +632,17 @@ __global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* part, int 
   pdl_trigger();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
-  if (c < cols)
-#pragma unroll 4
-    for (int p = threadIdx.y; p < parts; p += 32) v += part[static_cast<long long>(p) * cols + c];
+  if (c < cols) {
+    // sixteen loads at a time: the partials are few, and their latency is the kernel's time
+    for (int p0 = threadIdx.y; p0 < parts; p0 += 32 * 16) {
+      float t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        t[i] = p0 + 32 * i < parts ? part[static_cast<long long>(p0 + 32 * i) * cols + c] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v += t[i];
+    }
+  }
   sh[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = sh[threadIdx.x][threadIdx.y];
