@@ -328,7 +328,12 @@ msign_status pair_launch(PairParams* p, int64_t nz, double flops, double bytes, 
   const int64_t total = int64_t(p->tiles_m) * p->tiles_n * nz;
   if (total > INT32_MAX / 2) return MSIGN_ERR_UNSUPPORTED;
   p->total = static_cast<int>(total);
-  p->band = std::min(8, p->tiles_m);
+  // Tile rows walked together: as many as hold their A rows in about a
+  // quarter of the L2, so that B is read from HBM once a band (sustained,
+  // int8 8192 x 14336 x 4096: 8 rows 357 us, 16 343; gated block 4096 x 4096 x
+  // 14336: 734 and 720); at least 8, whose tiles share K slices in time.
+  const double panel = 256.0 * p->nk * p->segs * kRowBytes;
+  p->band = std::min(p->tiles_m, std::max(8, std::min(32, static_cast<int>(36e6 / panel))));
   p->err = dev->err;
   p->timeout_ns = kWaitLimitNs;
   const unsigned grid = 2 * static_cast<unsigned>(std::min<int64_t>(total, dev->max_pairs));
