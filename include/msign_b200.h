@@ -145,7 +145,9 @@ msign_status msign_sync_status(msign_stream_t stream);
  * of one kind and returns their count, summed device time in milliseconds,
  * FLOPs and bytes; msign_profile_reset() drops all records.  Kinds: 0 =
  * tensor-core GEMM, 1 = Frobenius-norm reduction, 2 = cast/orient/scale
- * ingest, 3 = Muon elementwise (momentum, weight update).  Not thread-safe
+ * ingest (and the layer products' operand copies), 3 = elementwise (Muon's
+ * momentum and weight update, the RMS norms, the gated block's activation
+ * gradients).  Not thread-safe
  * with concurrent library calls on other host threads.
  * ------------------------------------------------------------------------ */
 msign_status msign_profile_enable(int enable);

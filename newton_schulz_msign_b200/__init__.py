@@ -10,6 +10,7 @@ calling these without the built library or without a CUDA tensor raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from . import _lib
@@ -495,33 +496,54 @@ def _like(t, ref, name, shape=None, dtype=None):
     return t, _rows_layout(t, name)[2]
 
 
-def _call(fn, t, stream, *args):
-    """The status of an entry point called on t's device, with the stream
-    (default: that device's current stream) as its last argument."""
+def _on_stream(op):
+    """Runs the operator with its ``stream`` argument (a torch stream or a raw
+    handle) as the current stream, so that the outputs and the workspace that
+    it allocates belong to that stream too."""
+    @functools.wraps(op)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return op(*args, **kwargs)
+        torch = _torch()
+        t = args[0] if args else next(iter(kwargs.values()), None)
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            return op(*args, **kwargs)  # refused there
+        device = t.device
+        if not isinstance(stream, torch.cuda.Stream):
+            # (handle 0 would make ExternalStream take a new stream)
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the call runs on {device}")
+        with torch.cuda.stream(stream):
+            return op(*args, **kwargs)
+    call.__doc__ += "\n\n    ``stream``: the stream to run on, for the outputs too (default: the current one)."
+    return call
+
+
+def _call(fn, t, *args):
+    """The status of an entry point called on t's device, with that device's
+    current stream as its last argument."""
     torch = _torch()
     index = t.get_device()
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch.cuda.current_device() == index:
         return fn(*args, stream)
     with torch.cuda.device(index):
         return fn(*args, stream)
 
 
-def _call_with_workspace(fn, size_fn, size_args, t, workspace, stream, *args):
+def _call_with_workspace(fn, size_fn, size_args, t, workspace, *args):
     """_call with a workspace (pointer and bytes) behind args.  Operands that
     need none, the usual case, are called without asking; the entry point
     refuses before it enqueues anything where they do."""
     ws = workspace
     if ws is not None:
         _on(ws, t.get_device(), "workspace")
-        return _call(fn, t, stream, *args, ws.data_ptr(), ws.numel() * ws.element_size())
-    st = _call(fn, t, stream, *args, None, 0)
+        return _call(fn, t, *args, ws.data_ptr(), ws.numel() * ws.element_size())
+    st = _call(fn, t, *args, None, 0)
     if st == _lib.ERR_WORKSPACE:
         ws, wsb = _workspace(size_fn(*size_args), t.device, None)
-        st = _call(fn, t, stream, *args, ws.data_ptr(), wsb)
+        st = _call(fn, t, *args, ws.data_ptr(), wsb)
     return st
 
 
@@ -553,7 +575,8 @@ def _norm_inputs(x, residual, sum_out, index):
     return (rows, cols, xs, rs) + _like(sum_out, x, "sum_out")
 
 
-def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_out=None, stream=None):
+@_on_stream
+def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_out=None):
     """RMS norm of the last dim of ``x`` (bf16/fp16/fp32), after adding ``residual`` if one is given.
 
     Returns y = s * weight / sqrt(mean(s^2) + eps), or (y, s) with the sum
@@ -564,13 +587,13 @@ def rms_norm(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, sum_
     rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out, index)
     wdt, wp = _norm_weight(weight, x, index)
     y, ys = _like(out, x, "out")
-    check(_call(_lib.lib().rms_norm, x, stream, x.data_ptr(), _ptr(residual), wp, y.data_ptr(), _ptr(s), code, wdt, rows,
+    check(_call(_lib.lib().rms_norm, x, x.data_ptr(), _ptr(residual), wp, y.data_ptr(), _ptr(s), code, wdt, rows,
                 cols, xs, rs, ys, ss, eps), "rms_norm")
     return y if residual is None else (y, s)
 
 
-def rms_norm_q8(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, scale_out=None, sum_out=None,
-                stream=None):
+@_on_stream
+def rms_norm_q8(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, scale_out=None, sum_out=None):
     """``rms_norm`` with y quantised to int8, one float32 scale a row (max|y| / 127): returns
     (q, scale), or (q, scale, s) when there is a residual.  q * scale[..., None] is what it stands for."""
     torch = _torch()
@@ -578,10 +601,14 @@ def rms_norm_q8(x, weight=None, residual=None, *, eps: float = 1e-6, out=None, s
     rows, cols, xs, rs, s, ss = _norm_inputs(x, residual, sum_out, index)
     wdt, wp = _norm_weight(weight, x, index)
     q, qs = _like(out, x, "out", dtype=torch.int8)
-    scale, _ = _like(scale_out, x, "scale_out", shape=x.shape[:-1], dtype=torch.float32)
-    if scale_out is not None:
-        _need_cuda(scale, "scale_out")
-    check(_call(_lib.lib().rms_norm_q8, x, stream, x.data_ptr(), _ptr(residual), wp, q.data_ptr(), scale.data_ptr(),
+    if scale_out is None:
+        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    else:
+        scale = scale_out
+        _on(scale, index, "scale_out")
+        if scale.shape != x.shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous():
+            raise ValueError(f"scale_out must be contiguous float32 of shape {tuple(x.shape[:-1])}")
+    check(_call(_lib.lib().rms_norm_q8, x, x.data_ptr(), _ptr(residual), wp, q.data_ptr(), scale.data_ptr(),
                 _ptr(s), code, wdt, rows, cols, xs, rs, qs, ss, eps), "rms_norm_q8")
     return (q, scale) if residual is None else (q, scale, s)
 
@@ -590,8 +617,8 @@ def rms_norm_backward_workspace_size(rows: int, cols: int) -> int:
     return int(_lib.lib().rms_norm_backward_workspace_size(rows, cols))
 
 
-def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_out=None, dw_out=None, workspace=None,
-                      stream=None):
+@_on_stream
+def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_out=None, dw_out=None, workspace=None):
     """Gradients of ``rms_norm``: (dx, dw) from ``dy`` and ``s``, the sum that it returned (x without a residual).
 
     ``dsum``: the gradient that reaches s past the norm, added to dx.  dx is
@@ -610,13 +637,11 @@ def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_ou
     L = _lib.lib()
     dw, ws, wsb = None, None, 0
     if weight is not None:
-        dw, _ = _like(dw_out, weight, "dw_out")
-        if dw_out is not None:
-            _need_cuda(dw, "dw_out")
+        dw = _torch().empty_like(weight) if dw_out is None else _like(dw_out, weight, "dw_out")[0]
         ws, wsb = _workspace(L.rms_norm_backward_workspace_size(rows, cols), s.device, workspace)
     elif dw_out is not None:
         raise ValueError("dw_out needs a weight")
-    check(_call(L.rms_norm_backward, s, stream, dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
+    check(_call(L.rms_norm_backward, s, dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
                 wdt, rows, cols, strides[0], zs, strides[1], dxs, eps, _ptr(ws), wsb), "rms_norm_backward")
     return dx, dw
 
@@ -627,7 +652,8 @@ def i8_matmul_workspace_size(a, b) -> int:
     return int(_lib.lib().i8_matmul_workspace_size(m, n, k, a.data_ptr(), sa, b.data_ptr(), sb))
 
 
-def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=None, stream=None):
+@_on_stream
+def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=None):
     """(a b^T) of int8 ``a`` (..., k) and ``b`` (n, k), times float32 ``a_scale`` (...) for each row of a (token)
     and ``b_scale`` (n,) for each row of b (output channel).
 
@@ -652,7 +678,7 @@ def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=Non
     out, so = _like(out, a, "out", shape=a.shape[:-1] + (n,), dtype=out_dtype)
     code, L = _dtype_code(out), _lib.lib()
     pa, pb = a.data_ptr(), b.data_ptr()
-    check(_call_with_workspace(L.i8_matmul, L.i8_matmul_workspace_size, (m, n, k, pa, sa, pb, sb), a, workspace, stream, pa,
+    check(_call_with_workspace(L.i8_matmul, L.i8_matmul_workspace_size, (m, n, k, pa, sa, pb, sb), a, workspace, pa,
                                a_scale.data_ptr(), pb, b_scale.data_ptr(), out.data_ptr(), code, m, n, k, sa, sb, so),
           "i8_matmul")
     return out
@@ -689,8 +715,9 @@ def gated_ffn_workspace_size(x, w_gate, w_up) -> int:
     return int(_lib.lib().gated_ffn_workspace_size(t, d, h, x.data_ptr(), xs, w_gate.data_ptr(), w_up.data_ptr(), ws))
 
 
+@_on_stream
 def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, out=None, gate_out=None, up_out=None,
-              workspace=None, stream=None):
+              workspace=None):
     """act(x w_gate^T) * (x w_up^T) of ``x`` (..., d) and weights (h, d), bf16 or fp16, in one kernel.
 
     ``activation``: "silu", "gelu" or "gelu_tanh".  With ``save`` (or
@@ -712,7 +739,7 @@ def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, 
             raise ValueError("gate_out and up_out must have one row stride")
     L = _lib.lib()
     px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-    check(_call_with_workspace(L.gated_ffn, L.gated_ffn_workspace_size, (t, d, h, px, xs, pg, pu, sw), x, workspace, stream,
+    check(_call_with_workspace(L.gated_ffn, L.gated_ffn_workspace_size, (t, d, h, px, xs, pg, pu, sw), x, workspace,
                                px, pg, pu, out.data_ptr(), _ptr(gate), _ptr(up), code, act, t, d, h, xs, sw, so, sp),
           "gated_ffn")
     return (out, gate, up) if save else out
@@ -732,8 +759,9 @@ def gated_ffn_backward_workspace_size(x, w_gate, w_up) -> int:
                                                             w_up.data_ptr(), ws))
 
 
+@_on_stream
 def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu", grad_dtype=None, need_dx=True,
-                       need_dw=True, dx_out=None, dw_gate_out=None, dw_up_out=None, workspace=None, stream=None):
+                       need_dw=True, dx_out=None, dw_gate_out=None, dw_up_out=None, workspace=None):
     """Gradients of ``gated_ffn``: (dx, dw_gate, dw_up) from ``dh`` and the kept ``gate`` and ``up``.
 
     ``grad_dtype``: of the weight gradients, x's dtype (default) or float32;
@@ -767,7 +795,7 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu
     L = _lib.lib()
     px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
     ws, wsb = _workspace(L.gated_ffn_backward_workspace_size(t, d, h, px, xs, pg, pu, sw), x.device, workspace)
-    check(_call(L.gated_ffn_backward, x, stream, dh.data_ptr(), px, pg, pu, gate.data_ptr(), up.data_ptr(), _ptr(dx),
+    check(_call(L.gated_ffn_backward, x, dh.data_ptr(), px, pg, pu, gate.data_ptr(), up.data_ptr(), _ptr(dx),
                 _ptr(dwg), _ptr(dwu), code, _dtype_codes[grad_dtype], act, t, d, h, sdh, xs, sw, sp, sdx, sdw, _ptr(ws),
                 wsb), "gated_ffn_backward")
     return dx, dwg, dwu

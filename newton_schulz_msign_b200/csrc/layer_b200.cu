@@ -149,7 +149,8 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
 
 // Partial rows of dw that the gradients leave at most: four blocks an SM.
 constexpr int64_t kDwParts = 4 * kPlanSms;
-constexpr int64_t kDwLoopParts = 128;  // row chunks of the loop form
+constexpr int64_t kDwLoopParts = 128;  // row chunks of the loop form for rows whose sums shared memory does not hold
+constexpr int64_t kLoopSums = 12000;   // columns whose sums it does (48 KB without a raised limit)
 constexpr int kSmemMax = 232448;       // shared memory of a block
 constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has some static shared memory too)
 
@@ -180,10 +181,16 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char*
     st = launch(k, dim3(static_cast<unsigned>(parts)), dim3(x, y), static_cast<size_t>(stages) * slot, 0, 3, 0.0,
                 bytes, stream, a, stages);
     if (st != MSIGN_OK) return st;
+  } else if (dw != nullptr && a.cols <= kLoopSums && a.rows <= 2 * kDwParts) {
+    // few rows: one launch less (777 x 1001 fp32: 20 us a call with the host's part, 16 so; 16384 x 1001 93 us, 129 so)
+    parts = std::min<int64_t>(a.rows, kDwParts);
+    st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(parts)), dim3(256), sizeof(float) * a.cols, 0, 3,
+                0.0, bytes, stream, a, 1);
+    if (st != MSIGN_OK) return st;
   } else {
     a.rstd = dw != nullptr ? rstd : nullptr;
     st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
-                stream, a);
+                stream, a, 0);
     if (st != MSIGN_OK || dw == nullptr) return st;
     const int chunk = static_cast<int>(ceil_div(a.rows, std::min<int64_t>(a.rows, kDwLoopParts)));
     parts = ceil_div(a.rows, chunk);

@@ -577,33 +577,47 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   }
 }
 
-// Any width and alignment: dz and the row statistic, one row a block.
+// Any width and alignment, one row a block at a time.  With dynamic shared
+// memory for a row of dw (`sums`) the block takes every gridDim.x-th row and
+// leaves a partial row of dw like the kernel above (each thread adds to its
+// own columns only); else it leaves the row statistic for
+// rms_norm_dw_loop_kernel.
 template <typename T>
-__global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArgs a) {
+__global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArgs a, int sums) {
+  extern __shared__ float sdw[];  // [cols] with sums
   __shared__ float2 red[64];
   pdl_wait();
   pdl_trigger();
-  const long long row = blockIdx.x;
-  const T* z = static_cast<const T*>(a.z) + row * a.zs;
-  const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
-  float ss = 0.0f, dot = 0.0f;
-  for (int c = threadIdx.x; c < a.cols; c += 256) {
-    const float zv = Elem<T>::get(z[c]);
-    ss = fmaf(zv, zv, ss);
-    dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c), zv, dot);
+  if (sums)
+    for (int c = threadIdx.x; c < a.cols; c += 256) sdw[c] = 0.0f;
+  int par = 0;
+  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
+    const T* z = static_cast<const T*>(a.z) + row * a.zs;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
+    float ss = 0.0f, dot = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      const float zv = Elem<T>::get(z[c]);
+      ss = fmaf(zv, zv, ss);
+      dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c), zv, dot);
+    }
+    const float2 t = row_sum2(ss, dot, red, par);
+    const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
+    const float m = t.y * rstd / static_cast<float>(a.cols);
+    if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+    T* dz = static_cast<T*>(a.dz) + row * a.dzs;
+    const T* ds = a.ds == nullptr ? nullptr : static_cast<const T*>(a.ds) + row * a.dss;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      const float n = Elem<T>::get(z[c]) * rstd;
+      const float gv = Elem<T>::get(dy[c]);
+      const float d = rstd * fmaf(-n, m, gv * weight_at<T>(a.w, a.w_f32, c));
+      dz[c] = Elem<T>::put(ds != nullptr ? d + Elem<T>::get(ds[c]) : d);
+      if (sums) sdw[c] = fmaf(gv, n, sdw[c]);
+    }
   }
-  const float2 t = row_sum2(ss, dot, red, 0);
-  const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
-  const float m = t.y * rstd / static_cast<float>(a.cols);
-  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
-  T* dz = static_cast<T*>(a.dz) + row * a.dzs;
-  const T* ds = a.ds == nullptr ? nullptr : static_cast<const T*>(a.ds) + row * a.dss;
-  for (int c = threadIdx.x; c < a.cols; c += 256) {
-    const float n = Elem<T>::get(z[c]) * rstd;
-    const float g = Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c);
-    const float d = rstd * fmaf(-n, m, g);
-    dz[c] = Elem<T>::put(ds != nullptr ? d + Elem<T>::get(ds[c]) : d);
-  }
+  if (sums)
+    for (int c = threadIdx.x; c < a.cols; c += 256) a.part[static_cast<long long>(blockIdx.x) * a.cols + c] = sdw[c];
 }
 
 // Partial sums of dw over the rows of one chunk: thread = column, block row

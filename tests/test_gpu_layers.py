@@ -456,3 +456,112 @@ def test_two_streams_and_a_captured_graph():
     for a, (_, b) in zip(want, graphs):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
     msb.sync_status()
+
+
+def test_explicit_streams_and_more_dims():
+    x, wg, wu = ffn_inputs(24, 64, 96, BF16, 200)
+    w, dh = randn((64,), 203, BF16), randn((24, 96), 204, BF16)
+    q, b = i8((24, 64), 205), i8((40, 64), 206)
+    sa, sb = torch.rand(24, device="cuda"), torch.rand(40, device="cuda")
+
+    def run(v, **kw):
+        """The operators on inputs whose leading dims are those of v(tensor)."""
+        y, s = msb.rms_norm(v(x), w, v(x), **kw)
+        qq, sc, _ = msb.rms_norm_q8(x=v(x), weight=w, residual=v(x), **kw)
+        dx, dw = msb.rms_norm_backward(v(x), v(x), w, dsum=v(x), **kw)
+        z = msb.i8_matmul(v(q), v(sa), b, sb, **kw)
+        h, g, u = msb.gated_ffn(v(x), wg, wu, save=True, **kw)
+        return [y, s, qq, sc, dx, dw, z, h, g, u, *msb.gated_ffn_backward(v(dh), v(x), wg, wu, g, u, **kw)]
+
+    want = run(lambda t: t)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        got = run(lambda t: t, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, got))
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    for shape in ((2, 3, 4), (4, 6)):
+        got = run(lambda t: t.view(shape + t.shape[1:]))
+        assert got[0].shape == shape + (64,) and got[3].shape == shape and got[6].shape == shape + (40,)
+        assert all(torch.equal(a, c.view(a.shape)) for a, c in zip(want, got))
+    # a single row without a leading dim
+    y, dw = msb.rms_norm(x[3], w), msb.rms_norm_backward(x[3], x[3], w)[1]
+    assert y.shape == (64,) and dw.shape == (64,)
+    q1, s1 = msb.rms_norm_q8(x[3], w, scale_out=torch.empty((), device="cuda"))
+    assert s1.shape == () and msb.i8_matmul(q1, s1, b, sb).shape == (40,)
+    assert torch.equal(msb.gated_ffn(x[3], wg, wu), msb.gated_ffn(x[3:4], wg, wu)[0])
+
+
+def test_rows_beyond_32_bit_offsets():
+    # three rows 2^30 elements apart (the last at 2^31), and the same rows side by side
+    big = torch.empty(2 ** 31 + 4096, dtype=BF16, device="cuda")
+    far = lambda off, n: torch.as_strided(big, (3, n), (2 ** 30, 1), off)  # noqa: E731
+    x, dh = randn((3, 64), 210, BF16), randn((3, 96), 211, BF16)
+    wg, wu = randn((96, 64), 212, BF16, 0.1), randn((96, 64), 213, BF16, 0.1)
+    xf, df = far(0, 64), far(64, 96)
+    xf.copy_(x), df.copy_(dh)
+    w = randn((64,), 214, FP32)
+    y, s = msb.rms_norm(x, w, x)
+    yf, sf = msb.rms_norm(xf, w, xf, out=far(256, 64), sum_out=far(320, 64))
+    assert torch.equal(y, yf) and torch.equal(s, sf)
+    assert torch.equal(msb.rms_norm_backward(x, x, w)[0], msb.rms_norm_backward(xf, xf, w, dx_out=far(384, 64))[0])
+    h, g, u = msb.gated_ffn(x, wg, wu, save=True)
+    hf, gf, uf = msb.gated_ffn(xf, wg, wu, out=far(512, 96), gate_out=far(640, 96), up_out=far(768, 96))
+    assert torch.equal(h, hf) and torch.equal(g, gf) and torch.equal(u, uf)
+    a = msb.gated_ffn_backward(dh, x, wg, wu, g, u)
+    c = msb.gated_ffn_backward(df, xf, wg, wu, gf, uf, dx_out=far(1024, 64))
+    assert all(torch.equal(p, q) for p, q in zip(a, c))
+    # 600 rows through the kernels of many rows: out rows 2^22 elements apart
+    x6 = randn((600, 64), 215, BF16)
+    of = torch.as_strided(big, (512, 96), (2 ** 22, 1), 0)
+    msb.gated_ffn(x6[:512], wg.repeat(64, 1)[:96], wu, out=of)
+    assert torch.equal(of, msb.gated_ffn(x6[:512], wg, wu))
+    wide = randn((96 * 70, 64), 216, BF16, 0.1)
+    of = torch.as_strided(big, (512, 96 * 70), (2 ** 22, 1), 0)
+    msb.gated_ffn(x6[:512], wide, wide, out=of)
+    assert torch.equal(of, msb.gated_ffn(x6[:512], wide, wide))
+
+
+def test_a_given_workspace_and_a_small_one():
+    x, wg, wu = ffn_inputs(40, 73, 50, FP16, 220)  # rows that have to be copied
+    need = msb.gated_ffn_workspace_size(x, wg, wu)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(msb.gated_ffn(x, wg, wu, workspace=ws), msb.gated_ffn(x, wg, wu))
+    with pytest.raises(msb.MsignError):
+        msb.gated_ffn(x, wg, wu, workspace=ws[: need - 256])
+    a, b = i8((40, 73), 221), i8((50, 73), 222)
+    ws = torch.empty(msb.i8_matmul_workspace_size(a, b), dtype=torch.uint8, device="cuda")
+    one = torch.ones(50, device="cuda")
+    assert torch.equal(msb.i8_matmul(a, one[:40], b, one, workspace=ws), msb.i8_matmul(a, one[:40], b, one))
+    # a workspace that holds anything is fine: no call reads what an earlier one left
+    dh, gate, up = (randn((40, 50), s, FP16) for s in (223, 224, 225))
+    ws = torch.full((msb.gated_ffn_backward_workspace_size(x, wg, wu),), 255, dtype=torch.uint8, device="cuda")
+    got = msb.gated_ffn_backward(dh, x, wg, wu, gate, up, workspace=ws)
+    assert all(torch.equal(p, q) for p, q in zip(got, msb.gated_ffn_backward(dh, x, wg, wu, gate, up)))
+    s, dy, w = randn((40, 4096), 226, FP16), randn((40, 4096), 227, FP16), randn((4096,), 228, FP16)
+    ws = torch.full((msb.rms_norm_backward_workspace_size(40, 4096),), 255, dtype=torch.uint8, device="cuda")
+    got = msb.rms_norm_backward(dy, s, w, workspace=ws)
+    assert all(torch.equal(p, q) for p, q in zip(got, msb.rms_norm_backward(dy, s, w)))
+
+
+def test_the_largest_tiles_and_many_splits():
+    # shapes that reach every tile width and split of the few-row kernel, against the integer product
+    one = torch.ones(4200, device="cuda")
+    for m, n, k in ((1, 128, 8192), (16, 256, 4096), (30, 640, 2048), (64, 128, 16384), (65, 640, 4096), (100, 128, 9000),
+                    (129, 300, 2048), (150, 1000, 4096), (208, 512, 6000), (256, 256, 512), (300, 640, 2048),
+                    (450, 1000, 1024), (1500, 128, 300), (2500, 256, 4096)):
+        a, b = i8((m, k), m), i8((n, k), n)
+        got = msb.i8_matmul(a, one[:m], b, one[:n], out_dtype=FP32)
+        assert torch.equal(got, (a.double() @ b.double().T).float()), (m, n, k)
+
+
+@pytest.mark.parametrize("t,d,h", [(4000, 256, 256), (2100, 300, 200), (2048, 1000, 512), (200, 3000, 96), (1, 512, 8192)])
+def test_gated_ffn_backward_long_and_wide(t, d, h):
+    # long sums of the weight gradients (the split form), and outputs much wider than they are high
+    x, wg, wu = ffn_inputs(t, d, h, BF16, 230)
+    gate, up, dh = randn((t, h), 233, BF16), randn((t, h), 234, BF16), randn((t, h), 235, BF16)
+    got = msb.gated_ffn_backward(dh, x, wg, wu, gate, up)
+    want, mags, facs = L.ffn_backward(dh, x, wg, wu, gate, up, "silu")
+    ffn_grad_check(got, want, mags, facs, BF16, (BF16, BF16, BF16), (2 * h, t, t))
