@@ -796,12 +796,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
       for (int s = 0; s < p.splits; ++s, at += chunk * 32) add(at[0], GATED ? at[16] : at[0]);
     } else {
       const uint32_t at = smem_u32(part + (split * chunk + local) * 128 + c);
-      for (int s = 0; s < p.splits; s += 2) {  // (two or more ranks, a power of two)
-        const uint32_t a0 = mapa_shared(at, s), a1 = mapa_shared(at, s + 1);
-        const float4 f0 = ld_dsmem_f4(a0), f1 = ld_dsmem_f4(a1);
-        const float4 g0 = GATED ? ld_dsmem_f4(a0 + 256) : f0, g1 = GATED ? ld_dsmem_f4(a1 + 256) : f1;
-        add(f0, g0);
-        add(f1, g1);
+      // two or more ranks, a power of two: four loads on their way at a time
+      for (int s = 0; s < p.splits; s += 4) {
+        float4 f[4], g[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t from = mapa_shared(at, min(s + r, p.splits - 1));
+          f[r] = ld_dsmem_f4(from);
+          if (GATED) g[r] = ld_dsmem_f4(from + 256);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (s + r < p.splits) add(f[r], GATED ? g[r] : f[r]);
       }
     }
     const int n = p.N - (unit0 + c);

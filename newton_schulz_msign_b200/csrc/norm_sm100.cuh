@@ -196,10 +196,25 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2* red, int pa
   return make_float2(a, b);
 }
 
-// Largest |v| of a row, given as its bits: as whole numbers they order like
-// the magnitudes, with infinity and then NaN on top, so that a NaN is kept.
-__device__ __forceinline__ uint32_t row_max_bits(uint32_t m, uint32_t* red) {
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
+// Whether fp32 holds the mean of squares with all its digits.  Where it does
+// not (magnitudes past 1e15, or eps 0 and magnitudes below 1e-15), the row is
+// summed again times norm_rescale().
+__device__ __forceinline__ bool mean_holds(float ms) { return ms > 1e-30f && ms < 1e30f; }
+__device__ __forceinline__ float norm_rescale(float ms) {
+  return ms < 1.0f ? 7.922816251426434e28f : 1.262177448353619e-29f;  // 2^96, 2^-96
+}
+
+// max(|v|, m) that keeps a NaN of either.
+__device__ __forceinline__ float max_abs(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// Largest magnitude of a row (not negative, or NaN: as whole numbers the bits
+// order like the values, with infinity and then NaN on top).
+__device__ __forceinline__ float row_max(float v, uint32_t* red) {
+  uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
   const int nw = blockDim.x >> 5;
   if (nw > 1) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -207,21 +222,30 @@ __device__ __forceinline__ uint32_t row_max_bits(uint32_t m, uint32_t* red) {
     __syncthreads();
     m = __reduce_max_sync(0xFFFFFFFFu, lane < nw ? red[lane] : 0u);
   }
-  return m;
+  return __uint_as_float(m);
 }
 
-// The scale of an int8 row and the factor that takes y to q.  A row of zeros
-// has scale 0 and q = 0; one that holds an infinity or a NaN has that as its
-// scale and q = 0, so that what it stands for is NaN throughout.
-__device__ __forceinline__ float q8_factor(uint32_t amax_bits, float* scale) {
-  const float amax = __uint_as_float(amax_bits);
+// The scale of an int8 row and the factors that take y to q: q = rint((y
+// pre) f).  pre is 1 but for rows so small that 127 / max overflows.  A row
+// of zeros has scale 0 and q = 0; one that holds an infinity or a NaN has
+// that as its scale and q = 0 (f = 0 says so), so that what it stands for is
+// NaN throughout.
+__device__ __forceinline__ float q8_factor(float amax, float* scale, float* pre) {
   *scale = __fdiv_rn(amax, 127.0f);
-  return amax > 0.0f && amax_bits < 0x7F800000u ? __fdiv_rn(127.0f, amax) : 0.0f;
+  *pre = amax < 1e-30f ? 1.8446744073709552e19f : 1.0f;
+  if (!(amax > 0.0f) || __float_as_uint(amax) >= 0x7F800000u) return 0.0f;
+  return __fdiv_rn(127.0f, amax * *pre);
 }
 
-__device__ __forceinline__ int q8(float y, float f) {
-  const int q = __float2int_rn(y * f);  // NaN gives 0
-  return max(-127, min(127, q));
+// Four values to int8, packed.  Adding 1.5 2^23 rounds the sum to a whole
+// number (ties to even) and leaves it in the low mantissa bits: one fused
+// multiply-add a value instead of a conversion, a clamp and a mask (|y f| is
+// at most 127 and two roundings, which cannot reach 127.5).
+__device__ __forceinline__ uint32_t q8_pack(float a, float b, float c, float d, float f) {
+  constexpr float kRound = 12582912.0f;
+  const uint32_t x = __float_as_uint(fmaf(a, f, kRound)), y = __float_as_uint(fmaf(b, f, kRound));
+  const uint32_t z = __float_as_uint(fmaf(c, f, kRound)), w = __float_as_uint(fmaf(d, f, kRound));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 
 template <typename T>
@@ -289,7 +313,20 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
     for (int j = 0; j < V; ++j) ss = fmaf(v[j], v[j], ss);
   }
   ss = row_sum2(ss, 0.0f, red, 0).x;
-  const float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  if (!mean_holds(ss / static_cast<float>(a.cols) + a.eps)) {  // (the same for the whole row)
+    const float p = norm_rescale(ss / static_cast<float>(a.cols) + a.eps);
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float v[V];
+      Elem<T>::unpack(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(v[j] * p, v[j] * p, ss);
+    }
+    ss = row_sum2(ss, 0.0f, red, 1).x;
+    rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps * p * p) * p;
+  }
   if (!Q8) {
     T* y = static_cast<T*>(a.y) + row * a.ys;
 #pragma unroll
@@ -307,7 +344,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
   } else {
     int8_t* y = static_cast<int8_t*>(a.y) + row * a.ys;
     float v[VPT][V];
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
@@ -318,13 +355,19 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           v[i][j] = v[i][j] * rstd * w[j];
-          m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+          m = max_abs(m, v[i][j]);
         }
       }
     }
-    float scale;
-    const float f = q8_factor(row_max_bits(m, redm), &scale);
+    float scale, pre;
+    const float f = q8_factor(row_max(m, redm), &scale, &pre);
     if (threadIdx.x == 0) a.scale[row] = scale;
+    if (pre != 1.0f) {  // (the same for the whole row)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] *= pre;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
@@ -332,8 +375,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
         uint32_t p[V / 4];
 #pragma unroll
         for (int j = 0; j < V / 4; ++j)
-          p[j] = (q8(v[i][4 * j], f) & 255) | (q8(v[i][4 * j + 1], f) & 255) << 8 |
-                 (q8(v[i][4 * j + 2], f) & 255) << 16 | (q8(v[i][4 * j + 3], f) & 255) << 24;
+          p[j] = f == 0.0f ? 0u : q8_pack(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3], f);
         if (V == 8)
           *reinterpret_cast<uint2*>(y + c) = make_uint2(p[0], p[V / 4 - 1]);
         else
@@ -375,21 +417,30 @@ __global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
   }
   if (s != nullptr) x = s, r = nullptr;
   ss = row_sum2(ss, 0.0f, red, 0).x;
-  const float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  if (!mean_holds(ss / static_cast<float>(a.cols) + a.eps)) {
+    const float p = norm_rescale(ss / static_cast<float>(a.cols) + a.eps);
+    ss = 0.0f;
+    for (int c = threadIdx.x; c < a.cols; c += 256) ss = fmaf(z_at(c) * p, z_at(c) * p, ss);
+    ss = row_sum2(ss, 0.0f, red, 1).x;
+    rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps * p * p) * p;
+  }
   if (!Q8) {
     T* y = static_cast<T*>(a.y) + row * a.ys;
     for (int c = threadIdx.x; c < a.cols; c += 256)
       y[c] = Elem<T>::put(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c));
   } else {
     int8_t* y = static_cast<int8_t*>(a.y) + row * a.ys;
-    uint32_t m = 0;
+    float m = 0.0f;
     for (int c = threadIdx.x; c < a.cols; c += 256)
-      m = max(m, __float_as_uint(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c)) & 0x7FFFFFFFu);
-    float scale;
-    const float f = q8_factor(row_max_bits(m, redm), &scale);
+      m = max_abs(m, z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c));
+    float scale, pre;
+    const float f = q8_factor(row_max(m, redm), &scale, &pre);
     if (threadIdx.x == 0) a.scale[row] = scale;
-    for (int c = threadIdx.x; c < a.cols; c += 256)
-      y[c] = static_cast<int8_t>(q8(z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c), f));
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      const float v = z_at(c) * rstd * weight_at<T>(a.w, a.w_f32, c) * pre;
+      y[c] = f == 0.0f ? int8_t(0) : static_cast<int8_t>(q8_pack(v, 0.0f, 0.0f, 0.0f, f) & 0xFFu);
+    }
   }
 }
 
@@ -502,8 +553,29 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
         ss += f.x, dot += f.y;
       }
     }
-    const float rstd = rsqrtf(fmaf(ss, inv, a.eps));
-    const float m = -dot * rstd * inv;  // minus the mean of dy w n
+    float rstd = rsqrtf(fmaf(ss, inv, a.eps));
+    float m = -dot * rstd * inv;  // minus the mean of dy w n
+    if (mine && !mean_holds(fmaf(ss, inv, a.eps))) {
+      // (the same for the whole row) each warp sums the row by itself: no
+      // barrier that the block's other rows would have to meet
+      const float p = norm_rescale(fmaf(ss, inv, a.eps));
+      const T* zr = reinterpret_cast<const T*>(src);
+      const T* gr = reinterpret_cast<const T*>(src + ny * row_bytes);
+      ss = dot = 0.0f;
+      for (int c = lane; c < a.cols; c += 32) {
+        const float zp = Elem<T>::get(zr[c]) * p;
+        ss = fmaf(zp, zp, ss);
+        dot = fmaf(Elem<T>::get(gr[c]) * weight_at<T>(a.w, a.w_f32, c), zp, dot);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+      }
+      const float r = rsqrtf(fmaf(ss, inv, a.eps * p * p));
+      m = -dot * r * inv;
+      rstd = r * p;
+    }
     const f32x2 rstd2 = pair2(rstd, rstd), m2 = pair2(m, m);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -602,8 +674,23 @@ __global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArg
       dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c), zv, dot);
     }
     const float2 t = row_sum2(ss, dot, red, par);
-    const float rstd = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps);
-    const float m = t.y * rstd / static_cast<float>(a.cols);
+    const float ms = t.x / static_cast<float>(a.cols) + a.eps;
+    float rstd = __frsqrt_rn(ms);
+    float m = t.y * rstd / static_cast<float>(a.cols);
+    if (!mean_holds(ms)) {
+      const float p = norm_rescale(ms);
+      ss = dot = 0.0f;
+      for (int c = threadIdx.x; c < a.cols; c += 256) {
+        const float zp = Elem<T>::get(z[c]) * p;
+        ss = fmaf(zp, zp, ss);
+        dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(a.w, a.w_f32, c), zp, dot);
+      }
+      __syncthreads();  // every thread has read the first sums
+      const float2 t2 = row_sum2(ss, dot, red, par);
+      const float r = __frsqrt_rn(t2.x / static_cast<float>(a.cols) + a.eps * p * p);
+      m = t2.y * r / static_cast<float>(a.cols);
+      rstd = r * p;
+    }
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
     T* dz = static_cast<T*>(a.dz) + row * a.dzs;
     const T* ds = a.ds == nullptr ? nullptr : static_cast<const T*>(a.ds) + row * a.dss;

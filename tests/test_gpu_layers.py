@@ -80,6 +80,48 @@ def test_rms_norm_q8(dtype, shape, residual):
     assert L.worst(q, y / (amax / 127)[:, None], torch.tensor(0.5 + 127 * 2 * rel, device="cuda")) <= 1
 
 
+@pytest.mark.parametrize("dtype,tiny,big", [(BF16, 1e-38, 1e18), (FP16, 6e-8, 6e4), (FP32, 1e-40, 1e18)])
+@pytest.mark.parametrize("cols", [64, 77, 4096])
+def test_rms_norm_q8_at_the_ends_of_the_range(dtype, tiny, big, cols):
+    # rows of the smallest and largest magnitudes whose squares fp32 holds or loses, and weights that make y tiny or huge
+    x = randn((6, cols), 400 + cols, FP32)
+    x[0] = torch.where(x[0] > 0, tiny, -tiny)
+    x[1] = torch.where(x[1] > 0, big, -big)
+    x = x.to(dtype)
+    for scale in (1.0, 1e-38, 1e-30, 1e30):
+        w = randn((cols,), 500, FP32) * scale
+        q, s = msb.rms_norm_q8(x, w, eps=1e-6)
+        y = L.rms(x, w, 1e-6)
+        amax = y.abs().amax(1)
+        # fp32 flushes nothing here, but its subnormals carry fewer digits: 2^-149 absolute in y and in the scale
+        ok = amax / 127 > 2.0 ** -126
+        rel = 110 * 2.0 ** -24
+        assert L.worst(s[ok], (amax / 127)[ok], (amax / 127 * rel)[ok]) <= 1
+        assert int(q.abs().max()) <= 127 and bool((q[ok].abs().amax(1) == 127).all())
+        assert L.worst(q[ok], (y / (amax / 127)[:, None])[ok], torch.tensor(0.5 + 127 * 2 * rel, device="cuda")) <= 1
+        assert bool(torch.isfinite(s).all())
+
+
+@pytest.mark.parametrize("cols", [64, 77, 1024, 4096, 16384])
+def test_rms_norm_of_rows_whose_squares_leave_fp32(cols):
+    x = randn((7, cols), 600, FP32) * torch.tensor([1e18, 1e30, 1e-25, 1.0, 1e-38, 3e19, 1e37], device="cuda")[:, None]
+    x[1, 3] = 1e-30
+    w, dy = randn((cols,), 601, FP32), randn((7, cols), 602, FP32)
+    y = msb.rms_norm(x, w, eps=0.0)
+    want = L.rms(x, w, 0.0)
+    # as the ordinary rows, and 2^-149 absolute of rstd where the row is near the type's end (1e37: 2e-8 of rstd)
+    assert L.worst(y, want, want.abs() * (2.0 ** -24 + 400 * 2.0 ** -24) + 2.0 ** -126) <= 1
+    dx, dw = msb.rms_norm_backward(dy, x, w, eps=0.0)
+    wx, ww, mx, mw = L.rms_backward(dy, x, w, None, 0.0)
+    for i in range(7):
+        if float(mx[i].max()) < 1e38:
+            assert L.worst(dx[i], wx[i], mx[i] * 400 * 2.0 ** -24 + 2.0 ** -126) <= 1, i
+    assert L.worst(dw, ww, mw * 400 * 2.0 ** -24) <= 1
+    one = msb.rms_norm(x[:1].to(BF16), w, eps=1e-6)
+    want = L.rms(x[:1].to(BF16), w, 1e-6)
+    assert L.worst(one, want, want.abs() * (L.U[BF16] + 100 * 2.0 ** -24)) <= 1
+
+
 def test_rms_norm_without_weight_and_in_place():
     for cols in (512, 1003):
         x, r = randn((6, cols), 7, BF16), randn((6, cols), 8, BF16)
