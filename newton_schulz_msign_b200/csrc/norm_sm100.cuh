@@ -13,9 +13,9 @@
 // one pass over memory.  Sums and statistics are fp32; y is formed in fp32
 // and rounded once (int8: the fp32 y is quantised, never a rounded one).
 //
-// Rows whose addresses or width do not allow 16-byte accesses, and rows
-// longer than 1024 threads hold, take the *_loop kernels: element by element,
-// the row read again for each pass (it is still in L1 or L2 then).
+// Rows whose addresses or width do not allow 16-byte accesses move element by
+// element; rows longer than 1024 threads hold take the *_loop kernels, which
+// read the row again for each pass (it is still in L1 or L2 then).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -391,7 +391,99 @@ __device__ __forceinline__ float weight_at(const void* w, int w_f32, int c) {
   return w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::get(static_cast<const T*>(w)[c]);
 }
 
-// Any width and alignment: one row a block of 256 threads.  A thread reads
+// Any width and alignment, up to 8 elements a thread: like the kernel above
+// with single elements for pieces (element i of thread t is column i
+// blockDim.x + t, so that a warp's accesses lie side by side).
+constexpr int kNormElems = 8;
+
+template <typename T, bool Q8>
+__global__ void __launch_bounds__(kNormMaxThreads) rms_norm_elem_kernel(const NormArgs a) {
+  constexpr int E = kNormElems;
+  __shared__ float2 red[64];
+  __shared__ uint32_t redm[32];
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;  // (blocks of several rows have no barrier)
+  const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  float v[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    v[i] = c < a.cols ? Elem<T>::get(x[c]) : 0.0f;
+  }
+  if (a.r != nullptr) {
+    const T* r = static_cast<const T*>(a.r) + row * a.rs;
+    float rv[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      rv[i] = c < a.cols ? Elem<T>::get(r[c]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      const T sum = Elem<T>::put(v[i] + rv[i]);
+      v[i] = Elem<T>::get(sum);
+      if (c < a.cols && a.s != nullptr) static_cast<T*>(a.s)[row * a.ss + c] = sum;
+    }
+  }
+  float w[E];
+  if (a.w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = 1.0f;
+  } else if (a.w_f32) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      w[i] = c < a.cols ? static_cast<const float*>(a.w)[c] : 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      w[i] = c < a.cols ? Elem<T>::get(static_cast<const T*>(a.w)[c]) : 0.0f;
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) ss = fmaf(v[i], v[i], ss);
+  ss = row_sum2(ss, 0.0f, red, 0).x;
+  float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+  if (!mean_holds(ss / static_cast<float>(a.cols) + a.eps)) {
+    const float p = norm_rescale(ss / static_cast<float>(a.cols) + a.eps);
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss = fmaf(v[i] * p, v[i] * p, ss);
+    ss = row_sum2(ss, 0.0f, red, 1).x;
+    rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps * p * p) * p;
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = i * blockDim.x + threadIdx.x;
+    v[i] = v[i] * rstd * w[i];
+    if (Q8) {
+      if (c < a.cols) m = max_abs(m, v[i]);
+    } else if (c < a.cols) {
+      static_cast<T*>(a.y)[row * a.ys + c] = Elem<T>::put(v[i]);
+    }
+  }
+  if (Q8) {
+    float scale, pre;
+    const float f = q8_factor(row_max(m, redm), &scale, &pre);
+    if (threadIdx.x == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int c = i * blockDim.x + threadIdx.x;
+      if (c < a.cols)
+        static_cast<int8_t*>(a.y)[row * a.ys + c] =
+            f == 0.0f ? int8_t(0) : static_cast<int8_t>(q8_pack(v[i] * pre, 0.0f, 0.0f, 0.0f, f) & 0xFFu);
+    }
+  }
+}
+
+// Rows longer than that: one row a block of 256 threads.  A thread reads
 // back only what it wrote itself, so the sum may replace x or r in place.
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
