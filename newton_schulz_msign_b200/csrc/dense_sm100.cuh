@@ -566,7 +566,7 @@ struct StreamParams {
 };
 
 constexpr int kStreamThreads = 192;  // producer, MMA issuer, four epilogue warps
-constexpr int kStreamMaxStages = 12;
+constexpr int kStreamMaxStages = 8;
 constexpr int kStreamATile = 128 * kRowBytes;
 __host__ __device__ inline int stream_stage_bytes(int bn) { return kStreamATile + bn * kRowBytes; }
 // Behind the stages: the barriers, then (from the next 1024 bytes on) the join's own memory where it has some.

@@ -79,28 +79,25 @@ struct NormPlan {
 };
 
 // Threads for rows of `pieces` 16-byte pieces: up to 128 pieces a warp takes
-// a row (no block barrier), beyond that a block does.
-NormPlan norm_plan(int64_t pieces, int rows_per_block, int block_vpt, int max_threads, int max_vpt) {
+// a row (no block barrier) and a block four, beyond that a block takes one.
+NormPlan norm_plan(int64_t pieces) {
   NormPlan p;
+  if (pieces > int64_t(kNormMaxThreads) * kNormVpt) return p;
+  p.vec = true;
   if (pieces <= 32 * kNormVpt) {
-    p.vec = true;
     p.vpt = pieces <= 32 ? 1 : pieces <= 64 ? 2 : 4;
-    p.block = dim3(32, rows_per_block);
+    p.block = dim3(32, 4);
     return p;
   }
-  int vpt = block_vpt;
-  while (vpt < max_vpt && pieces > int64_t(max_threads) * vpt) vpt *= 2;
-  if (pieces > int64_t(max_threads) * vpt) return p;
-  p.vec = true;
-  p.vpt = vpt;
-  p.block = dim3(static_cast<unsigned>(round_up(ceil_div(pieces, vpt), 32)), 1);
+  p.vpt = pieces <= 2 * kNormMaxThreads ? 2 : kNormVpt;
+  p.block = dim3(static_cast<unsigned>(round_up(ceil_div(pieces, p.vpt), 32)), 1);
   return p;
 }
 
 template <typename T, bool Q8>
 msign_status norm_run(const NormArgs& a, bool vec_ok, double bytes, cudaStream_t stream) {
   NormPlan p;
-  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec, 4, 2, kNormMaxThreads, kNormVpt);
+  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec);
   // Measured, elements in registers against the loop form, 8192 rows with a
   // residual: 101 columns bf16 6.7 and 14.1 us, 2001 63 and 65, 4099 135 and
   // 116; 4099 fp32 118 and 131.
@@ -176,6 +173,8 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char*
   const int row_bytes = a.cols * static_cast<int>(sizeof(T));
   const int arrays = a.ds != nullptr ? 3 : 2;
   if (vec_ok && pieces <= kNormBwdThreads * kNormBwdVpt) {
+    // as few pieces a thread as 256 threads a row allow, the block filled up
+    // with rows, and the ring as deep as the SM's blocks leave room for
     int vpt = pieces <= 32 ? 1 : 2;
     while (pieces > vpt * kNormBwdThreads) vpt *= 2;
     const int x = static_cast<int>(round_up(ceil_div(pieces, vpt), 32));
@@ -185,8 +184,11 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char*
     int stages = std::min(kNormRing, kNormRingMax / per_sm / slot);
     while (stages < 2) stages = std::min(kNormRing, kNormRingMax / --per_sm / slot);
     parts = std::min<int64_t>({ceil_div(a.rows, y), int64_t(kPlanSms) * per_sm, kDwParts});  // what the workspace holds
-    auto* k = vpt == 1 ? rms_norm_bwd_kernel<T, 1> : vpt == 2 ? rms_norm_bwd_kernel<T, 2>
-              : vpt == 4 ? rms_norm_bwd_kernel<T, 4> : rms_norm_bwd_kernel<T, 8>;
+    const bool full = pieces == int64_t(x) * vpt;
+    auto* k = vpt == 1   ? (full ? rms_norm_bwd_kernel<T, 1, true> : rms_norm_bwd_kernel<T, 1, false>)
+              : vpt == 2 ? (full ? rms_norm_bwd_kernel<T, 2, true> : rms_norm_bwd_kernel<T, 2, false>)
+              : vpt == 4 ? (full ? rms_norm_bwd_kernel<T, 4, true> : rms_norm_bwd_kernel<T, 4, false>)
+                         : (full ? rms_norm_bwd_kernel<T, 8, true> : rms_norm_bwd_kernel<T, 8, false>);
     st = launch(k, dim3(static_cast<unsigned>(parts)), dim3(x, y), static_cast<size_t>(stages) * slot, 0, 3, 0.0,
                 bytes, stream, a, stages);
     if (st != MSIGN_OK) return st;
@@ -289,11 +291,13 @@ msign_status smem_limit(K kernel, int bytes) {
 
 template <typename T>
 msign_status norm_bwd_limits() {
-  msign_status st = smem_limit(rms_norm_bwd_kernel<T, 1>, kNormRingMax);
-  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 2>, kNormRingMax);
-  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 4>, kNormRingMax);
-  if (st == MSIGN_OK) st = smem_limit(rms_norm_bwd_kernel<T, 8>, kNormRingMax);
-  return st;
+  for (msign_status st :
+       {smem_limit(rms_norm_bwd_kernel<T, 1, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 1, false>, kNormRingMax),
+        smem_limit(rms_norm_bwd_kernel<T, 2, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 2, false>, kNormRingMax),
+        smem_limit(rms_norm_bwd_kernel<T, 4, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 4, false>, kNormRingMax),
+        smem_limit(rms_norm_bwd_kernel<T, 8, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 8, false>, kNormRingMax)})
+    if (st != MSIGN_OK) return st;
+  return MSIGN_OK;
 }
 
 std::mutex g_layer_mu;
@@ -359,22 +363,24 @@ msign_status pair_launch(PairParams* p, int64_t nz, double flops, double bytes, 
 
 // Whether a product of `rows` x `cols` outputs (`z` of them) goes to the
 // stream kernel: few rows, or too few 256-row tiles to keep the CTA pairs
-// busy.
+// busy.  Measured, stream and pair in us: int8 64 x 14336 x 4096 16.5 and 18.8,
+// 128 x 14336 x 4096 20.0 and 19.6, 256 x 14336 x 4096 (56 tiles) 26 and 18,
+// 256 x 4096 x 14336 (16 tiles) 21.4 and 39; gated 128 x 4096 x 14336 48 and
+// 56, 256 x 4096 x 14336 81 and 57, 256 x 4096 x 4096 (32 tiles) 22 and 28.
 template <int MODE>
 bool stream_takes(int64_t rows, int64_t cols, int64_t z) {
   return rows <= 128 || ceil_div(rows, kBM) * ceil_div(cols, MODE == PAIR_GATED ? 128 : kBN) * z < 48;
 }
-
 
 // Tile of a stream launch: the N operand's width (output rows a tile), the K
 // splits (the cluster's width) and the shared memory of a CTA.  The least of
 // an estimate in microseconds: the loads (each stage's 128 + bn rows of 128
 // bytes) at 120 KB/us on the busiest SM and 100 on the average one, 0.02 a row
 // of the tile for the join and the store, 1 and a quarter a rank for a join
-// between ranks, and 3 for every further generation of CTAs.  Measured against single choices for
-// all: tiles of at most 128 rows lose 22% on the 400 x 1000 x 2736 gated block
-// (18.7 against 14.5 us), tiles of 256 rows 25% on 256 x 4096 x 4096 int8
-// (15 against 11.8).
+// between ranks, and 3 for every further generation of CTAs.  Measured against
+// single choices for all: tiles of at most 128 rows lose 22% on the 400 x 1000
+// x 2736 gated block (18.7 against 14.5 us), tiles of 256 rows 25% on 256 x
+// 4096 x 4096 int8 (15 against 11.8).
 struct StreamPlan {
   int bn, splits, budget;
 };
@@ -385,8 +391,11 @@ StreamPlan stream_plan(int64_t rows, int64_t cols, int64_t z, int64_t steps) {
   const int64_t tiles = ceil_div(cols, MODE == PAIR_GATED ? 64 : 128) * z;
   StreamPlan best = {};
   double least = 0.0;
+  int64_t tried = 0;
   for (int64_t wide : {256, 192, 160, 128, 96, 64}) {
     const int64_t bn = round_up(ceil_div(rows, ceil_div(rows, wide)), unit);  // equal tiles
+    if (bn == tried) continue;
+    tried = bn;
     const int64_t per_sm = bn <= 128 ? 2 : 1;  // by shared memory
     for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
       const int64_t ctas = tiles * ceil_div(rows, bn) * splits;
@@ -413,6 +422,9 @@ msign_status stream_launch(StreamParams* p, const StreamPlan& plan, int64_t z, d
   if (tiles > INT32_MAX / 16 || rows > 65535) return MSIGN_ERR_UNSUPPORTED;
   p->bn = plan.bn;
   p->splits = plan.splits;
+  // A CTA's share of an SM's TMEM (512 columns) never exceeds its share of the
+  // shared memory: allocations then fit wherever the CTAs do, and no CTA waits
+  // for one that waits, in its cluster, for another.
   p->tmem_cols = 32;
   while (p->tmem_cols < p->bn) p->tmem_cols *= 2;
   // what a rank holds of the sums
@@ -423,11 +435,13 @@ msign_status stream_launch(StreamParams* p, const StreamPlan& plan, int64_t z, d
   // pulled sums lie where the stages were
   while (!p->push && p->stages * stream_stage_bytes(p->bn) < p->bn * 512) ++p->stages;
   p->join_off = stream_join_off(p->bn, p->stages);
+  const int smem = p->stages * stream_stage_bytes(p->bn) + fixed;
+  if (smem > kSmemMax || int64_t(smem) * 512 < int64_t(kSmemMax) * p->tmem_cols) return MSIGN_ERR_UNSUPPORTED;
   p->err = dev->err;
   p->timeout_ns = kWaitLimitNs;
   return launch(dense_stream_kernel<MODE>,
                 dim3(static_cast<unsigned>(tiles * p->splits), static_cast<unsigned>(rows), static_cast<unsigned>(z)),
-                dim3(kStreamThreads), p->stages * stream_stage_bytes(p->bn) + fixed, p->splits, 0, flops, bytes, stream, *p);
+                dim3(kStreamThreads), smem, p->splits, 0, flops, bytes, stream, *p);
 }
 
 // Output pointers and row strides of a stream launch.

@@ -131,6 +131,12 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   return r;
 }
 
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack2(const uint4& u, f32x2 (&v)[Elem<T>::vec / 2]) {
   float f[Elem<T>::vec];
@@ -538,6 +544,25 @@ __global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
 
 // ---------------------------------------------------------------- gradients
 
+// Sums of (z p)^2 and dy w z p over a row, by one warp.  A call of its own:
+// inlined, the rare case's registers made the common one spill (8192 x 4096
+// with ds 62 us, 56 so; without ds 56 and 49).
+template <typename T>
+__device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w, int w_f32, int cols, float p) {
+  float ss = 0.0f, dot = 0.0f;
+  for (int c = threadIdx.x & 31; c < cols; c += 32) {
+    const float zp = Elem<T>::get(z[c]) * p;
+    ss = fmaf(zp, zp, ss);
+    dot = fmaf(Elem<T>::get(dy[c]) * weight_at<T>(w, w_f32, c), zp, dot);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  }
+  return make_float2(ss, dot);
+}
+
 // Persistent: a block takes blockDim.y rows at a time, blockDim.x threads
 // each (whole warps; piece i of thread t starts at column (i blockDim.x + t)
 // vec), block b the row groups b, b + gridDim.x, ...  The rows' dy, z and ds
@@ -551,7 +576,7 @@ __global__ void __launch_bounds__(256) rms_norm_loop_kernel(const NormArgs a) {
 // blocks).
 constexpr int kNormRing = 8;
 
-template <typename T, int VPT>
+template <typename T, int VPT, bool FULL>
 __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1)
     rms_norm_bwd_kernel(const NormBwdArgs a, int stages) {
   constexpr int V = Elem<T>::vec, H = V / 2;
@@ -615,7 +640,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (mine && c < a.cols) {
+      if (mine && (FULL || c < a.cols)) {
         f32x2 zv[H], gv[H];
         rz[i] = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
         ry[i] = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
@@ -629,21 +654,24 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
       }
     }
     float ss = unpair2(ss2).x + unpair2(ss2).y, dot = unpair2(dot2).x + unpair2(dot2).y;
+    // the lower half of the warp joins ss, the upper half dot
+    float v = (lane < 16 ? ss : dot) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? dot : ss, 16);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-    }
-    if (lane == 0) red[par][warp] = make_float2(ss, dot);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if ((lane & 15) == 0) reinterpret_cast<float*>(&red[par][warp])[lane >> 4] = v;
     __syncthreads();
     // (past the barrier: the slot of the group before is free)
     if (warp == 0 && last >= 0 && row0 + (stages - 1) * step < a.rows) fill(row0 + (stages - 1) * step, last);
-    if (nwarp > 1) {  // every thread adds the row's warps up, in their order
-      ss = dot = 0.0f;
-      for (int i = 0; i < nwarp; ++i) {
-        const float2 f = red[par][warp0 + i];
-        ss += f.x, dot += f.y;
+    {  // every thread adds the row's warps up, in their order
+      const f32x2* r = reinterpret_cast<const f32x2*>(&red[par][warp0]);
+      f32x2 t = r[0];
+      if (nwarp == 8) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) t = add2(t, r[i]);
+      } else {
+        for (int i = 1; i < nwarp; ++i) t = add2(t, r[i]);
       }
+      ss = unpair2(t).x, dot = unpair2(t).y;
     }
     float rstd = rsqrtf(fmaf(ss, inv, a.eps));
     float m = -dot * rstd * inv;  // minus the mean of dy w n
@@ -651,28 +679,17 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
       // (the same for the whole row) each warp sums the row by itself: no
       // barrier that the block's other rows would have to meet
       const float p = norm_rescale(fmaf(ss, inv, a.eps));
-      const T* zr = reinterpret_cast<const T*>(src);
-      const T* gr = reinterpret_cast<const T*>(src + ny * row_bytes);
-      ss = dot = 0.0f;
-      for (int c = lane; c < a.cols; c += 32) {
-        const float zp = Elem<T>::get(zr[c]) * p;
-        ss = fmaf(zp, zp, ss);
-        dot = fmaf(Elem<T>::get(gr[c]) * weight_at<T>(a.w, a.w_f32, c), zp, dot);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      }
-      const float r = rsqrtf(fmaf(ss, inv, a.eps * p * p));
-      m = -dot * r * inv;
+      const float2 t = warp_sums<T>(reinterpret_cast<const T*>(src), reinterpret_cast<const T*>(src + ny * row_bytes),
+                                    a.w, a.w_f32, a.cols, p);
+      const float r = rsqrtf(fmaf(t.x, inv, a.eps * p * p));
+      m = -t.y * r * inv;
       rstd = r * p;
     }
     const f32x2 rstd2 = pair2(rstd, rstd), m2 = pair2(m, m);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (mine && c < a.cols) {
+      if (mine && (FULL || c < a.cols)) {
         f32x2 zv[H], gv[H], sv[H];
         unpack2<T>(rz[i], zv);
         unpack2<T>(ry[i], gv);
