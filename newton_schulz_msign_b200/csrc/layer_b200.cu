@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "dense_sm100.cuh"
@@ -70,6 +71,15 @@ bool rows_aligned(const void* p, int64_t stride, int64_t rows, int es) {
   return aligned16(p) && (rows <= 1 || (stride * es) % 16 == 0);
 }
 
+// Whether an output is one of the other buffers of its call (the same
+// address: the overlap that a slip makes; nullptr matches nothing).
+bool is_one_of(const void* p, std::initializer_list<const void*> others) {
+  if (p == nullptr) return false;
+  for (const void* o : others)
+    if (o == p) return true;
+  return false;
+}
+
 // ---------------------------------------------------------------- RMS norm
 
 struct NormPlan {
@@ -125,6 +135,9 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
       !valid_stride(s_stride, cols))
     return MSIGN_ERR_INVALID_ARG;
   if (residual == nullptr && sum_out != nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (rows > 0 && cols > 0 &&
+      (is_one_of(y, {sum_out, weight}) || is_one_of(sum_out, {weight}) || (q8 && is_one_of(y, {x, residual}))))
+    return MSIGN_ERR_INVALID_ARG;
   if (weight != nullptr && w_dtype != io_dtype && w_dtype != MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return MSIGN_OK;
   if (x == nullptr || y == nullptr) return MSIGN_ERR_INVALID_ARG;
@@ -574,6 +587,7 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   const int wdt = to_dt(w_dtype);
   if (rows == 0) return zero_rows(dw, cols, 1, cols, dtype_size(wdt), s);  // a sum over no rows
   if (dy == nullptr || sum == nullptr || dx == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (is_one_of(dx, {dy, sum, weight, dsum, dw}) || is_one_of(dw, {dy, sum, weight, dsum})) return MSIGN_ERR_INVALID_ARG;
   if (dw != nullptr && !workspace_ok(workspace, workspace_bytes, rms_norm_backward_workspace_size(rows, cols)))
     return MSIGN_ERR_WORKSPACE;
   DeviceState* dev = nullptr;
@@ -700,6 +714,9 @@ msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void
     return MSIGN_OK;
   }
   if (x == nullptr || w_gate == nullptr || w_up == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (is_one_of(out, {x, w_gate, w_up, gate_out, up_out}) || is_one_of(gate_out, {x, w_gate, w_up, up_out}) ||
+      is_one_of(up_out, {x, w_gate, w_up}))
+    return MSIGN_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes,
                     gated_ffn_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))
     return MSIGN_ERR_WORKSPACE;
@@ -782,6 +799,9 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
     return zero_rows(dw_up, lddw, h, d, dtype_size(gdt), stream);
   }
   if (dh == nullptr || x == nullptr || w_gate == nullptr || w_up == nullptr || gate == nullptr || up == nullptr)
+    return MSIGN_ERR_INVALID_ARG;
+  if (is_one_of(dx, {dh, x, w_gate, w_up, gate, up, dw_gate, dw_up}) ||
+      is_one_of(dw_gate, {dh, x, w_gate, w_up, gate, up, dw_up}) || is_one_of(dw_up, {dh, x, w_gate, w_up, gate, up}))
     return MSIGN_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes,
                     gated_ffn_backward_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))

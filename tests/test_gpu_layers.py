@@ -607,3 +607,35 @@ def test_gated_ffn_backward_long_and_wide(t, d, h):
     got = msb.gated_ffn_backward(dh, x, wg, wu, gate, up)
     want, mags, facs = L.ffn_backward(dh, x, wg, wu, gate, up, "silu")
     ffn_grad_check(got, want, mags, facs, BF16, (BF16, BF16, BF16), (2 * h, t, t))
+
+
+@pytest.mark.parametrize("t", [5, 300])
+def test_rows_behind_the_last_stay(t):
+    # outputs that are the first rows of larger tensors, in every kernel's range
+    def room(shape, dtype=BF16):
+        big = torch.full((shape[0] + 40, shape[1]), 5.0, device="cuda").to(dtype)
+        return big, big[:shape[0]]
+
+    x, wg, wu = ffn_inputs(t, 136, 264, BF16, 300)
+    dh, w = randn((t, 264), 303, BF16), randn((136,), 304, FP32)
+    bigs = []
+
+    def new(*shape, dtype=BF16):
+        big, v = room(shape, dtype)
+        bigs.append((big, shape[0]))
+        return v
+
+    s = new(t, 136)
+    msb.rms_norm(x, w, x, out=new(t, 136), sum_out=s)
+    msb.rms_norm_q8(x, w, out=new(t, 136, dtype=torch.int8))
+    msb.rms_norm_backward(x, s, w, dx_out=new(t, 136))
+    g, u = new(t, 264), new(t, 264)
+    msb.gated_ffn(x, wg, wu, out=new(t, 264), gate_out=g, up_out=u)
+    msb.gated_ffn_backward(dh, x, wg, wu, g, u, dx_out=new(t, 136), dw_gate_out=new(264, 136), dw_up_out=new(264, 136))
+    q = i8((t, 136), 305)
+    one = torch.ones(t, device="cuda")
+    for dtype in (BF16, FP32):
+        msb.i8_matmul(q, one, q, one, out=new(t, t, dtype=dtype))
+    msb.sync_status()
+    for big, rows in bigs:
+        assert bool((big[rows:] == 5).all()) and not bool((big[:rows] == 5).all())

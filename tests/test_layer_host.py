@@ -14,13 +14,19 @@ BAD, UNS, WS, OK = _lib.ERR_INVALID_ARG, _lib.ERR_UNSUPPORTED, _lib.ERR_WORKSPAC
 P = 1 << 20  # an address that no refused call touches
 
 
+def at(i):
+    """Another such address."""
+    return P + (i << 16)
+
+
+
 @pytest.fixture(scope="module")
 def lib():
     build.build()
     return _lib.lib()
 
 
-def norm(lib, x=P, r=None, w=P, y=P, s=None, io=B, wd=B, rows=4, cols=64, xs=0, rs=0, ys=0, ss=0, eps=1e-6):
+def norm(lib, x=P, r=None, w=at(1), y=at(2), s=None, io=B, wd=B, rows=4, cols=64, xs=0, rs=0, ys=0, ss=0, eps=1e-6):
     return lib.rms_norm(x, r, w, y, s, io, wd, rows, cols, xs, rs, ys, ss, eps, None)
 
 
@@ -29,14 +35,14 @@ def norm(lib, x=P, r=None, w=P, y=P, s=None, io=B, wd=B, rows=4, cols=64, xs=0, 
     (dict(eps=float("nan")), BAD), (dict(eps=float("inf")), BAD), (dict(xs=63), BAD), (dict(rs=-1), BAD), (dict(ys=1), BAD),
     (dict(ss=63), BAD), (dict(s=P), BAD), (dict(x=None), BAD), (dict(y=None), BAD), (dict(wd=H), UNS), (dict(io=F, wd=B), UNS),
     (dict(rows=2 ** 30 + 1), UNS), (dict(cols=2 ** 30 + 1), UNS), (dict(rows=0), OK), (dict(cols=0), OK),
-    (dict(rows=0, x=None, y=None), OK)])
+    (dict(rows=0, x=None, y=None), OK), (dict(r=at(3), s=at(2)), BAD), (dict(w=at(2)), BAD), (dict(r=at(3), s=at(1)), BAD)])
 def test_rms_norm_statuses(lib, kw, status):
     assert norm(lib, **kw) == status
 
 
 def test_rms_norm_q8_statuses(lib):
-    call = lambda scale=P, rows=4, q=P: lib.rms_norm_q8(P, None, P, q, scale, None, B, B, rows, 64, 0, 0, 0, 0, 1e-6, None)  # noqa: E731
-    assert call(scale=None) == BAD and call(q=None) == BAD and call(rows=0, scale=None) == OK
+    call = lambda scale=at(3), rows=4, q=at(2): lib.rms_norm_q8(P, None, at(1), q, scale, None, B, B, rows, 64, 0, 0, 0, 0, 1e-6, None)  # noqa: E731
+    assert call(scale=None) == BAD and call(q=None) == BAD and call(rows=0, scale=None) == OK and call(q=P) == BAD
 
 
 def test_rms_norm_backward_statuses(lib):
@@ -45,7 +51,7 @@ def test_rms_norm_backward_statuses(lib):
     # the partial sums do not grow with the rows beyond a fixed number of blocks
     assert lib.rms_norm_backward_workspace_size(10 ** 6, 64) < 4 * 10 ** 6 + 2 ** 20
 
-    def call(dy=P, s=P, w=P, ds=None, dx=P, dw=P, io=B, wd=B, rows=4, cols=64, st=(0, 0, 0, 0), eps=1e-6, ws=P, wsb=need):
+    def call(dy=P, s=at(1), w=at(2), ds=None, dx=at(3), dw=at(4), io=B, wd=B, rows=4, cols=64, st=(0, 0, 0, 0), eps=1e-6, ws=P, wsb=need):
         return lib.rms_norm_backward(dy, s, w, ds, dx, dw, io, wd, rows, cols, *st, eps, ws, wsb, None)
 
     assert call(dy=None) == BAD and call(s=None) == BAD and call(dx=None) == BAD and call(io=9) == BAD
@@ -54,6 +60,7 @@ def test_rms_norm_backward_statuses(lib):
         assert call(st=tuple(32 if j == i else 0 for j in range(4))) == BAD
     assert call(ws=None) == WS and call(wsb=need - 1) == WS and call(ws=P + 16) == WS
     assert call(cols=0) == OK and call(rows=0, dw=None) == OK
+    assert call(dx=P) == BAD and call(dx=at(1)) == BAD and call(ds=at(5), dx=at(5)) == BAD and call(dw=at(2)) == BAD and call(dw=at(3)) == BAD
 
 
 def test_i8_matmul_statuses(lib):
@@ -74,7 +81,7 @@ def test_i8_matmul_statuses(lib):
 
 
 def ffn_args(lib, **kw):
-    d = dict(x=P, wg=P, wu=P, out=P, g=None, u=None, dt=B, act=0, t=4, d=64, h=64, st=(0, 0, 0, 0), ws=None, wsb=0)
+    d = dict(x=P, wg=at(1), wu=at(2), out=at(3), g=None, u=None, dt=B, act=0, t=4, d=64, h=64, st=(0, 0, 0, 0), ws=None, wsb=0)
     d.update(kw)
     return lib.gated_ffn(d["x"], d["wg"], d["wu"], d["out"], d["g"], d["u"], d["dt"], d["act"], d["t"], d["d"], d["h"],
                          *d["st"], d["ws"], d["wsb"], None)
@@ -85,7 +92,8 @@ def ffn_args(lib, **kw):
     (dict(dt=3), BAD), (dict(act=3), BAD), (dict(act=-1), BAD), (dict(t=-1), BAD), (dict(d=-1), BAD), (dict(h=-1), BAD),
     (dict(st=(63, 0, 0, 0)), BAD), (dict(st=(0, 63, 0, 0)), BAD), (dict(st=(0, 0, 63, 0)), BAD), (dict(st=(0, 0, 0, 63)), BAD),
     (dict(dt=F), UNS), (dict(t=2 ** 30 + 1), UNS), (dict(d=2 ** 30 + 1), UNS), (dict(h=2 ** 30 + 1), UNS),
-    (dict(d=65), WS), (dict(x=P + 2), WS), (dict(wu=P + 8), WS), (dict(st=(65, 0, 0, 0)), WS), (dict(st=(0, 68, 0, 0)), WS),
+    (dict(d=65), WS), (dict(x=P + 2), WS), (dict(wu=P + 8), WS),
+    (dict(out=P), BAD), (dict(out=at(1)), BAD), (dict(g=at(3), u=at(4)), BAD), (dict(g=at(4), u=at(4)), BAD), (dict(st=(65, 0, 0, 0)), WS), (dict(st=(0, 68, 0, 0)), WS),
     (dict(t=0), OK), (dict(h=0, out=None), OK)])
 def test_gated_ffn_statuses(lib, kw, status):
     assert ffn_args(lib, **kw) == status
@@ -97,7 +105,7 @@ def test_gated_ffn_backward_statuses(lib):
     assert lib.gated_ffn_backward_workspace_size(4, 65, 64, P, 0, P, P, 0) >= need + 2 * 72 * (4 + 128)
     assert lib.gated_ffn_backward_workspace_size(0, 64, 64, P, 0, P, P, 0) == 0
 
-    def call(dh=P, x=P, wg=P, wu=P, g=P, u=P, dx=P, dg=P, du=P, dt=B, gd=B, act=0, t=4, d=64, h=64, st=(0,) * 6, ws=P, wsb=need):
+    def call(dh=P, x=at(1), wg=at(2), wu=at(3), g=at(4), u=at(5), dx=at(6), dg=at(7), du=at(8), dt=B, gd=B, act=0, t=4, d=64, h=64, st=(0,) * 6, ws=P, wsb=need):
         return lib.gated_ffn_backward(dh, x, wg, wu, g, u, dx, dg, du, dt, gd, act, t, d, h, *st, ws, wsb, None)
 
     for kw in (dict(dh=None), dict(x=None), dict(wg=None), dict(wu=None), dict(g=None), dict(u=None), dict(dg=None),
@@ -107,6 +115,8 @@ def test_gated_ffn_backward_statuses(lib):
         assert call(st=tuple(32 if j == i else 0 for j in range(6))) == BAD
     assert call(dt=F) == UNS and call(gd=H) == UNS and call(h=2 ** 30 + 1) == UNS
     assert call(ws=None) == WS and call(wsb=need - 1) == WS and call(ws=P + 64) == WS
+    for kw in (dict(dx=P), dict(dx=at(1)), dict(dg=at(2)), dict(du=at(7)), dict(dg=at(6)), dict(du=at(5))):
+        assert call(**kw) == BAD, kw
     assert call(d=0) == OK and call(t=0, dx=None, dg=P, du=P, h=0) == OK
 
 
