@@ -478,6 +478,14 @@ def _on(t, index, name):
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
 
 
+def _operand(t, index, name, shape, dtype):
+    """The row stride of an input that must have this shape, dtype and device."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} of {dtype}")
+    _on(t, index, name)
+    return 0 if t.is_contiguous() else _rows_layout(t, name)[2]
+
+
 def _like(t, ref, name, shape=None, dtype=None):
     """The given output, checked, or a new one: like ``ref`` but for shape and
     dtype; and its row stride."""
@@ -568,10 +576,7 @@ def _norm_inputs(x, residual, sum_out, index):
         if sum_out is not None:
             raise ValueError("sum_out needs a residual")
         return rows, cols, xs, 0, None, 0
-    _on(residual, index, "residual")
-    if residual.shape != x.shape or residual.dtype != x.dtype:
-        raise ValueError("residual must match x in shape and dtype")
-    rs = 0 if residual.is_contiguous() else _rows_layout(residual, "residual")[2]
+    rs = _operand(residual, index, "residual", x.shape, x.dtype)
     return (rows, cols, xs, rs) + _like(sum_out, x, "sum_out")
 
 
@@ -625,13 +630,8 @@ def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_ou
     the gradient of x and of the residual alike; dw is None without a weight."""
     code, index = _dtype_code(s), s.get_device()
     rows, cols, zs = _rows_layout(s, "s")
-    strides = []
-    for t, nm in ((dy, "dy"), (dsum, "dsum")):
-        if t is not None:
-            _on(t, index, nm)
-            if t.shape != s.shape or t.dtype != s.dtype:
-                raise ValueError(f"{nm} must match s in shape and dtype")
-        strides.append(0 if t is None or t.is_contiguous() else _rows_layout(t, nm)[2])
+    sdy = _operand(dy, index, "dy", s.shape, s.dtype)
+    sds = 0 if dsum is None else _operand(dsum, index, "dsum", s.shape, s.dtype)
     wdt, wp = _norm_weight(weight, s, index)
     dx, dxs = _like(dx_out, s, "dx_out")
     L = _lib.lib()
@@ -642,7 +642,7 @@ def rms_norm_backward(dy, s, weight=None, *, dsum=None, eps: float = 1e-6, dx_ou
     elif dw_out is not None:
         raise ValueError("dw_out needs a weight")
     check(_call(L.rms_norm_backward, s, dy.data_ptr(), s.data_ptr(), wp, _ptr(dsum), dx.data_ptr(), _ptr(dw), code,
-                wdt, rows, cols, strides[0], zs, strides[1], dxs, eps, _ptr(ws), wsb), "rms_norm_backward")
+                wdt, rows, cols, sdy, zs, sds, dxs, eps, _ptr(ws), wsb), "rms_norm_backward")
     return dx, dw
 
 
@@ -696,16 +696,13 @@ def _activation_code(name) -> int:
 def _ffn_inputs(x, w_gate, w_up):
     """(tokens, d, h, x stride, weight stride) of a gated block's inputs."""
     t, d, xs = _rows_layout(x, "x")
-    if w_gate.dim() != 2 or w_gate.shape != w_up.shape:
-        raise ValueError("w_gate and w_up must be (h, d) of one shape")
-    if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
-        raise TypeError("w_gate and w_up must be of x's dtype")
-    index = x.get_device()
-    _on(w_gate, index, "w_gate")
-    _on(w_up, index, "w_up")
-    h, _, sg = _rows_layout(w_gate, "w_gate", d)
-    su = _rows_layout(w_up, "w_up")[2]
-    if h > 1 and (sg or d) != (su or d):
+    shape = w_gate.shape
+    if len(shape) != 2 or shape[1] != d:
+        raise ValueError(f"w_gate must be (h, {d})")
+    h, index = shape[0], x.get_device()
+    sg = _operand(w_gate, index, "w_gate", shape, x.dtype)
+    su = _operand(w_up, index, "w_up", shape, x.dtype)
+    if sg != su and h > 1 and (sg or d) != (su or d):
         raise ValueError("w_gate and w_up must have one row stride")
     return t, d, h, xs, sg
 
@@ -745,14 +742,6 @@ def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, 
     return (out, gate, up) if save else out
 
 
-def _one_stride(a, an, b, bn, cols):
-    """The row stride that two matrices share."""
-    sa, sb = (_rows_layout(t, nm)[2] or cols for t, nm in ((a, an), (b, bn)))
-    if sa != sb:
-        raise ValueError(f"{an} and {bn} must have one row stride")
-    return sa
-
-
 def gated_ffn_backward_workspace_size(x, w_gate, w_up) -> int:
     t, d, h, xs, ws = _ffn_inputs(x, w_gate, w_up)
     return int(_lib.lib().gated_ffn_backward_workspace_size(t, d, h, x.data_ptr(), xs, w_gate.data_ptr(),
@@ -773,12 +762,10 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu
     if not need_dx and not need_dw:
         raise ValueError("at least one of need_dx and need_dw")
     shape, index = x.shape[:-1] + (h,), x.get_device()
-    for g, nm in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        _on(g, index, nm)
-        if g.shape != shape or g.dtype != x.dtype:
-            raise ValueError(f"{nm} must be {tuple(shape)} of x's dtype")
-    sdh = _rows_layout(dh, "dh")[2]
-    sp = _one_stride(gate, "gate", up, "up", h)
+    sdh = _operand(dh, index, "dh", shape, x.dtype)
+    sp, su = _operand(gate, index, "gate", shape, x.dtype), _operand(up, index, "up", shape, x.dtype)
+    if sp != su and (sp or h) != (su or h):
+        raise ValueError("gate and up must have one row stride")
     if grad_dtype is None:
         grad_dtype = x.dtype if dw_gate_out is None else dw_gate_out.dtype
     if grad_dtype not in (x.dtype, torch.float32):
@@ -788,8 +775,9 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu
     if need_dx:
         dx, sdx = _like(dx_out, x, "dx_out")
     if need_dw:
-        dwg, sdw = _like(dw_gate_out, w_gate, "dw_gate_out", dtype=grad_dtype)
-        dwu, su = _like(dw_up_out, w_up, "dw_up_out", dtype=grad_dtype)
+        other = None if grad_dtype == x.dtype else grad_dtype
+        dwg, sdw = _like(dw_gate_out, w_gate, "dw_gate_out", dtype=other)
+        dwu, su = _like(dw_up_out, w_up, "dw_up_out", dtype=other)
         if (sdw or d) != (su or d):
             raise ValueError("dw_gate_out and dw_up_out must have one row stride")
     L = _lib.lib()
