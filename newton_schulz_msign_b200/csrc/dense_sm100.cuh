@@ -874,15 +874,27 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
 
 // Rows of `cols` elements copied to rows of ld_out elements (a 16-byte
 // multiple), the rest zero: what a tensor map needs where the caller's rows
-// do not start on 16-byte boundaries.  U: the element as a whole number.
+// do not start on 16-byte boundaries.  One launch for up to three matrices
+// (blockIdx.y).  U: the element as a whole number.  HBM-bound; the loads are
+// single elements, side by side across a warp.
+struct PadArgs {
+  const void* in[3];
+  void* out[3];
+  long long ld_in[3], ld_out[3], rows[3];
+  int cols[3];
+};
+
 template <typename U>
-__global__ void __launch_bounds__(256) pad_rows_kernel(const U* in, long long ld_in, U* out, long long ld_out,
-                                                       long long rows, int cols) {
+__global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int V = 16 / sizeof(U);
-  const long long per = ld_out / V;
-  const long long total = rows * per;
+  const int m = blockIdx.y;
+  const U* in = static_cast<const U*>(a.in[m]);
+  U* out = static_cast<U*>(a.out[m]);
+  const long long ld_in = a.ld_in[m], ld_out = a.ld_out[m], per = ld_out / V;
+  const int cols = a.cols[m];
+  const long long total = a.rows[m] * per;
   for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 256ll * gridDim.x) {
     const long long r = i / per;
     const int c = static_cast<int>(i - r * per) * V;

@@ -268,22 +268,31 @@ struct Operand {
 
 void carve_operand(Carver& cv, const Operand& o, void** copy) { *copy = o.direct() ? nullptr : cv.take(o.padded_bytes()); }
 
-msign_status place_operand(Operand* o, void* copy, cudaStream_t stream) {
-  if (copy == nullptr) return MSIGN_OK;
-  const int64_t ldp = o->padded_ld();
-  const int64_t pieces = o->rows * (ldp * o->es / 16);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(pieces, 256), 16 * kPlanSms)));
-  const double bytes = 2.0 * o->rows * o->cols * o->es;
-  const msign_status st =
-      o->es == 1 ? launch(pad_rows_kernel<uint8_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes, stream,
-                          static_cast<const uint8_t*>(o->p), o->ld, static_cast<uint8_t*>(copy), ldp, o->rows,
-                          static_cast<int>(o->cols))
-                 : launch(pad_rows_kernel<uint16_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes, stream,
-                          static_cast<const uint16_t*>(o->p), o->ld, static_cast<uint16_t*>(copy), ldp, o->rows,
-                          static_cast<int>(o->cols));
-  o->p = copy;
-  o->ld = ldp;
-  return st;
+// Copies the operands that have a place for it (copies[i] not null), all in
+// one launch, and points them there.
+msign_status place_operands(std::initializer_list<Operand*> ops, std::initializer_list<void*> copies,
+                            cudaStream_t stream) {
+  PadArgs a = {};
+  int n = 0, es = 0;
+  int64_t most = 0;
+  double bytes = 0.0;
+  auto copy = copies.begin();
+  for (Operand* o : ops) {
+    void* to = *copy++;
+    if (to == nullptr) continue;
+    es = o->es;
+    a.in[n] = o->p, a.ld_in[n] = o->ld, a.out[n] = to, a.ld_out[n] = o->padded_ld();
+    a.rows[n] = o->rows, a.cols[n] = static_cast<int>(o->cols);
+    most = std::max(most, o->rows * (o->padded_ld() * es / 16));
+    bytes += 2.0 * o->rows * o->cols * es;
+    o->p = to;
+    o->ld = o->padded_ld();
+    ++n;
+  }
+  if (n == 0) return MSIGN_OK;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(most, 256), 16 * kPlanSms)), static_cast<unsigned>(n));
+  return launch(es == 1 ? pad_rows_kernel<uint8_t> : pad_rows_kernel<uint16_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes,
+                stream, a);
 }
 
 // Instruction descriptor: D type (fp32 or int32), A and B types, which of
@@ -646,8 +655,7 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
     void *ca, *cb;
     carve_operand(cv, oa, &ca);
     carve_operand(cv, ob, &cb);
-    if ((st = place_operand(&oa, ca, stream)) != MSIGN_OK) return st;
-    if ((st = place_operand(&ob, cb, stream)) != MSIGN_OK) return st;
+    if ((st = place_operands({&oa, &ob}, {ca, cb}, stream)) != MSIGN_OK) return st;
   }
   const double flops = 2.0 * m * n * k;
   const double bytes = static_cast<double>(m) * k + static_cast<double>(n) * k + static_cast<double>(oes) * m * n;
@@ -727,9 +735,7 @@ msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void
     Carver cv(carve_base(workspace));
     FfnCopies c;
     carve_ffn(cv, s, ox, og, ou, false, &c);
-    if ((st = place_operand(&ox, c.x, stream)) != MSIGN_OK) return st;
-    if ((st = place_operand(&og, c.wg, stream)) != MSIGN_OK) return st;
-    if ((st = place_operand(&ou, c.wu, stream)) != MSIGN_OK) return st;
+    if ((st = place_operands({&ox, &og, &ou}, {c.x, c.wg, c.wu}, stream)) != MSIGN_OK) return st;
   }
   const int dt = to_dt(dtype);
   const CUtensorMapDataType type = tma_type(dt, false);
@@ -812,9 +818,10 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
   Carver cv(carve_base(workspace));
   FfnCopies c;
   carve_ffn(cv, s, ox, og, ou, true, &c);
-  if (dw_gate != nullptr && (st = place_operand(&ox, c.x, stream)) != MSIGN_OK) return st;
-  if (dx != nullptr && (st = place_operand(&og, c.wg, stream)) != MSIGN_OK) return st;
-  if (dx != nullptr && (st = place_operand(&ou, c.wu, stream)) != MSIGN_OK) return st;
+  // (x feeds the weights' gradients only, the weights feed dx only)
+  st = place_operands({&ox, &og, &ou}, {dw_gate != nullptr ? c.x : nullptr, dx != nullptr ? c.wg : nullptr,
+                                        dx != nullptr ? c.wu : nullptr}, stream);
+  if (st != MSIGN_OK) return st;
   st = dt == DT_BF16 ? dact_run<__nv_bfloat16>(dh, ldh, gate, up, ldpre, c.dgu, s, act, stream)
                      : dact_run<__half>(dh, ldh, gate, up, ldpre, c.dgu, s, act, stream);
   if (st != MSIGN_OK) return st;
