@@ -540,18 +540,18 @@ def _call(fn, t, *args):
         return fn(*args, stream)
 
 
-def _call_with_workspace(fn, size_fn, size_args, t, workspace, *args):
-    """_call with a workspace (pointer and bytes) behind args.  Operands that
-    need none, the usual case, are called without asking; the entry point
-    refuses before it enqueues anything where they do."""
+def _call_with_workspace(fn, size_fn, size_args, plain, t, workspace, *args):
+    """_call with a workspace (pointer and bytes) behind args.  Where the width
+    looks ``plain``, the usual case, the entry point is called without asking
+    for a size; it refuses before it enqueues anything where it needs one."""
     ws = workspace
     if ws is not None:
         _on(ws, t.get_device(), "workspace")
         return _call(fn, t, *args, ws.data_ptr(), ws.numel() * ws.element_size())
-    st = _call(fn, t, *args, None, 0)
+    st = _call(fn, t, *args, None, 0) if plain else _lib.ERR_WORKSPACE
     if st == _lib.ERR_WORKSPACE:
         ws, wsb = _workspace(size_fn(*size_args), t.device, None)
-        st = _call(fn, t, *args, ws.data_ptr(), wsb)
+        st = _call(fn, t, *args, _ptr(ws), wsb)
     return st
 
 
@@ -678,9 +678,9 @@ def i8_matmul(a, a_scale, b, b_scale, *, out=None, out_dtype=None, workspace=Non
     out, so = _like(out, a, "out", shape=a.shape[:-1] + (n,), dtype=out_dtype)
     code, L = _dtype_code(out), _lib.lib()
     pa, pb = a.data_ptr(), b.data_ptr()
-    check(_call_with_workspace(L.i8_matmul, L.i8_matmul_workspace_size, (m, n, k, pa, sa, pb, sb), a, workspace, pa,
-                               a_scale.data_ptr(), pb, b_scale.data_ptr(), out.data_ptr(), code, m, n, k, sa, sb, so),
-          "i8_matmul")
+    check(_call_with_workspace(L.i8_matmul, L.i8_matmul_workspace_size, (m, n, k, pa, sa, pb, sb), k % 16 == 0, a,
+                               workspace, pa, a_scale.data_ptr(), pb, b_scale.data_ptr(), out.data_ptr(), code, m, n, k,
+                               sa, sb, so), "i8_matmul")
     return out
 
 
@@ -736,8 +736,8 @@ def gated_ffn(x, w_gate, w_up, *, activation: str = "silu", save: bool = False, 
             raise ValueError("gate_out and up_out must have one row stride")
     L = _lib.lib()
     px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
-    check(_call_with_workspace(L.gated_ffn, L.gated_ffn_workspace_size, (t, d, h, px, xs, pg, pu, sw), x, workspace,
-                               px, pg, pu, out.data_ptr(), _ptr(gate), _ptr(up), code, act, t, d, h, xs, sw, so, sp),
+    check(_call_with_workspace(L.gated_ffn, L.gated_ffn_workspace_size, (t, d, h, px, xs, pg, pu, sw), d % 8 == 0, x,
+                               workspace, px, pg, pu, out.data_ptr(), _ptr(gate), _ptr(up), code, act, t, d, h, xs, sw, so, sp),
           "gated_ffn")
     return (out, gate, up) if save else out
 

@@ -104,18 +104,26 @@ NormPlan norm_plan(int64_t pieces) {
   return p;
 }
 
+// Threads of the *_elem kernels: a warp a row where that holds it, four rows a
+// block; else a block a row.
+dim3 elem_block(int64_t cols, int pair) {
+  const int x = static_cast<int>(round_up(ceil_div(cols, pair * kNormElems), 32));
+  return dim3(x, x == 32 ? 4 : 1);
+}
+
+// pair: the elements that one access may move where 16 bytes may not (1 or 2).
 template <typename T, bool Q8>
-msign_status norm_run(const NormArgs& a, bool vec_ok, double bytes, cudaStream_t stream) {
+msign_status norm_run(const NormArgs& a, bool vec_ok, int pair, double bytes, cudaStream_t stream) {
   NormPlan p;
   if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec);
-  // Measured, elements in registers against the loop form, 8192 rows with a
-  // residual: 101 columns bf16 6.7 and 14.1 us, 2001 63 and 65, 4099 135 and
-  // 116; 4099 fp32 118 and 131.
-  if (!p.vec && a.cols <= kNormElems * (sizeof(T) == 4 ? kNormMaxThreads : 256)) {
-    // a warp a row up to 256 columns, four rows a block; beyond that a block a row
-    const int x = static_cast<int>(round_up(ceil_div(a.cols, kNormElems), 32)), y = x == 32 ? 4 : 1;
-    return launch(rms_norm_elem_kernel<T, Q8>, dim3(static_cast<unsigned>(ceil_div(a.rows, y))), dim3(x, y), 0, 0, 3, 0.0,
-                  bytes, stream, a);
+  // Measured, the row in registers against the loop form, 8192 rows with a
+  // residual: two elements an access, bf16, 1002 columns 23 and 31 us, 4098 93
+  // and 109; fp32 4586 107 and 124; one element, bf16, 101 columns 6.7 and
+  // 14.1, 2001 63 and 65, 4099 135 and 116.
+  if (!p.vec && a.cols <= pair * kNormElems * kNormMaxThreads && (pair == 2 || sizeof(T) == 4 || a.cols <= 2048)) {
+    const dim3 block = elem_block(a.cols, pair);
+    return launch(pair == 2 ? rms_norm_elem_kernel<T, 2, Q8> : rms_norm_elem_kernel<T, 1, Q8>,
+                  dim3(static_cast<unsigned>(ceil_div(a.rows, block.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
   }
   if (!p.vec)
     return launch(rms_norm_loop_kernel<T, Q8>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
@@ -152,18 +160,26 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
   a.rows = rows, a.cols = static_cast<int>(cols), a.eps = eps;
   a.w_f32 = w_dtype == MSIGN_FP32;
   const int dt = to_dt(io_dtype), es = dtype_size(dt), v = 16 / es;
-  bool vec = cols % v == 0 && rows_aligned(x, a.xs, rows, es) && (weight == nullptr || aligned16(weight)) &&
-             (residual == nullptr || rows_aligned(residual, a.rs, rows, es)) &&
-             (sum_out == nullptr || rows_aligned(sum_out, a.ss, rows, es));
-  vec = vec && (q8 ? reinterpret_cast<uintptr_t>(y) % v == 0 && (rows <= 1 || a.ys % v == 0)
-                   : rows_aligned(y, a.ys, rows, es));
+  // whether accesses of n elements reach every row of every matrix
+  const auto reach = [&](int n) {
+    const auto in = [&](const void* p, int64_t stride, int size) {
+      return p == nullptr ||
+             (reinterpret_cast<uintptr_t>(p) % (n * size) == 0 && (rows <= 1 || stride % n == 0));
+    };
+    // (a weight of fp32 is read 16 bytes at a time too)
+    const int ws = std::min(16, n * (a.w_f32 ? 4 : es));
+    return cols % n == 0 && in(x, a.xs, es) && in(residual, a.rs, es) && in(sum_out, a.ss, es) &&
+           in(y, a.ys, q8 ? 1 : es) && reinterpret_cast<uintptr_t>(weight) % ws == 0;
+  };
+  const bool vec = reach(v);
+  const int pair = reach(2) ? 2 : 1;
   const double e = static_cast<double>(rows) * cols;
   const double bytes = e * es * (1 + (residual != nullptr) + (sum_out != nullptr)) + e * (q8 ? 1 : es);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dt == DT_BF16)
-    return q8 ? norm_run<__nv_bfloat16, true>(a, vec, bytes, s) : norm_run<__nv_bfloat16, false>(a, vec, bytes, s);
-  if (dt == DT_FP16) return q8 ? norm_run<__half, true>(a, vec, bytes, s) : norm_run<__half, false>(a, vec, bytes, s);
-  return q8 ? norm_run<float, true>(a, vec, bytes, s) : norm_run<float, false>(a, vec, bytes, s);
+    return q8 ? norm_run<__nv_bfloat16, true>(a, vec, pair, bytes, s) : norm_run<__nv_bfloat16, false>(a, vec, pair, bytes, s);
+  if (dt == DT_FP16) return q8 ? norm_run<__half, true>(a, vec, pair, bytes, s) : norm_run<__half, false>(a, vec, pair, bytes, s);
+  return q8 ? norm_run<float, true>(a, vec, pair, bytes, s) : norm_run<float, false>(a, vec, pair, bytes, s);
 }
 
 // Partial rows of dw that the gradients leave at most: four blocks an SM.
@@ -174,7 +190,7 @@ constexpr int kSmemMax = 232448;       // shared memory of a block
 constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has some static shared memory too)
 
 template <typename T>
-msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char* ws, double bytes,
+msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, int pair, char* ws, double bytes,
                           cudaStream_t stream) {
   Carver cv(ws);
   float* part = static_cast<float*>(cv.take(sizeof(float) * std::min<int64_t>(a.rows, kDwParts) * a.cols));
@@ -206,21 +222,30 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, char*
                 bytes, stream, a, stages);
     if (st != MSIGN_OK) return st;
   } else if (dw != nullptr && a.cols <= kLoopSums && a.rows <= 2 * kDwParts) {
-    // few rows: one launch less (777 x 1001 fp32: 20 us a call with the host's part, 16 so; 16384 x 1001 93 us, 129 so)
+    // few rows: one launch less (777 x 1001 fp32: 20 us a call with the host's
+    // part, 17 so; 16384 x 1001 129 us, and 93 with the sums of dw apart)
     parts = std::min<int64_t>(a.rows, kDwParts);
     st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(parts)), dim3(256), sizeof(float) * a.cols, 0, 3,
                 0.0, bytes, stream, a, 1);
     if (st != MSIGN_OK) return st;
   } else {
     a.rstd = dw != nullptr ? rstd : nullptr;
-    st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
-                stream, a, 0);
+    // the row in registers (8192 x 1002 bf16 46 us, by the loop 76; 4098 175
+    // and 249)
+    if (a.cols <= pair * kNormElems * kNormBwdElemThreads) {
+      const dim3 block = elem_block(a.cols, pair);
+      st = launch(pair == 2 ? rms_norm_bwd_elem_kernel<T, 2> : rms_norm_bwd_elem_kernel<T, 1>,
+                  dim3(static_cast<unsigned>(ceil_div(a.rows, block.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
+    } else {
+      st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
+                  stream, a, 0);
+    }
     if (st != MSIGN_OK || dw == nullptr) return st;
     const int chunk = static_cast<int>(ceil_div(a.rows, std::min<int64_t>(a.rows, kDwLoopParts)));
     parts = ceil_div(a.rows, chunk);
-    st = launch(rms_norm_dw_loop_kernel<T>,
-                dim3(static_cast<unsigned>(ceil_div(a.cols, 128)), static_cast<unsigned>(parts)), dim3(128), 0, 0, 3,
-                0.0, 0.0, stream, a, chunk);
+    st = launch(pair == 2 ? rms_norm_dw_kernel<T, 2> : rms_norm_dw_kernel<T, 1>,
+                dim3(static_cast<unsigned>(ceil_div(a.cols, 128 * pair)), static_cast<unsigned>(parts)), dim3(128), 0, 0,
+                3, 0.0, 0.0, stream, a, chunk);
     if (st != MSIGN_OK) return st;
   }
   if (dw == nullptr) return MSIGN_OK;
@@ -608,14 +633,22 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   a.dss = stride_of(dsum_stride, cols), a.dzs = stride_of(dx_stride, cols);
   a.rows = rows, a.cols = static_cast<int>(cols), a.w_f32 = w_dtype == MSIGN_FP32, a.eps = eps;
   a.err = dev->err, a.timeout_ns = kWaitLimitNs;
-  const bool vec = cols % v == 0 && rows_aligned(dy, a.dys, rows, es) && rows_aligned(sum, a.zs, rows, es) &&
-                   rows_aligned(dx, a.dzs, rows, es) && (dsum == nullptr || rows_aligned(dsum, a.dss, rows, es)) &&
-                   (weight == nullptr || aligned16(weight));
+  const auto reach = [&](int n) {  // (see norm_call)
+    const auto in = [&](const void* p, int64_t stride) {
+      return p == nullptr ||
+             (reinterpret_cast<uintptr_t>(p) % (n * es) == 0 && (rows <= 1 || stride % n == 0));
+    };
+    const int wsz = std::min(16, n * (a.w_f32 ? 4 : es));
+    return cols % n == 0 && in(dy, a.dys) && in(sum, a.zs) && in(dsum, a.dss) && in(dx, a.dzs) &&
+           reinterpret_cast<uintptr_t>(weight) % wsz == 0;
+  };
+  const bool vec = reach(v);
+  const int pair = reach(2) ? 2 : 1;
   const double bytes = static_cast<double>(rows) * cols * es * (3 + (dsum != nullptr));
   char* ws = dw != nullptr ? carve_base(workspace) : nullptr;
-  if (dt == DT_BF16) return norm_bwd_run<__nv_bfloat16>(a, dw, wdt, vec, ws, bytes, s);
-  if (dt == DT_FP16) return norm_bwd_run<__half>(a, dw, wdt, vec, ws, bytes, s);
-  return norm_bwd_run<float>(a, dw, wdt, vec, ws, bytes, s);
+  if (dt == DT_BF16) return norm_bwd_run<__nv_bfloat16>(a, dw, wdt, vec, pair, ws, bytes, s);
+  if (dt == DT_FP16) return norm_bwd_run<__half>(a, dw, wdt, vec, pair, ws, bytes, s);
+  return norm_bwd_run<float>(a, dw, wdt, vec, pair, ws, bytes, s);
 }
 
 // ---------------------------------------------------------------- int8 product

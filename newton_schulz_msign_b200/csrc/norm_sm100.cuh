@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "gemm_sm100.cuh"
 #include "ptx_sm100.cuh"
@@ -401,12 +402,55 @@ __device__ __forceinline__ float weight_at(const void* w, int w_f32, int c) {
   return w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::get(static_cast<const T*>(w)[c]);
 }
 
-// Any width and alignment, up to 8 elements a thread: like the kernel above
-// with single elements for pieces (element i of thread t is column i
-// blockDim.x + t, so that a warp's accesses lie side by side).
+// P consecutive elements (1 or 2), as floats.  Two move as one access, which
+// their address has to allow.
+template <typename T, int P>
+__device__ __forceinline__ void load_p(const T* p, float (&v)[P]) {
+  if (P == 1) {
+    v[0] = Elem<T>::get(p[0]);
+  } else if (sizeof(T) == 4) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    v[0] = f.x, v[P - 1] = f.y;
+  } else {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    const uint16_t h[2] = {static_cast<uint16_t>(u), static_cast<uint16_t>(u >> 16)};
+    v[0] = Elem<T>::get(*reinterpret_cast<const T*>(&h[0]));
+    v[P - 1] = Elem<T>::get(*reinterpret_cast<const T*>(&h[1]));
+  }
+}
+
+template <typename T, int P>
+__device__ __forceinline__ void store_p(T* p, const float (&v)[P]) {
+  if (P == 1) {
+    p[0] = Elem<T>::put(v[0]);
+  } else if (sizeof(T) == 4) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[P - 1]);
+  } else {
+    const T h[2] = {Elem<T>::put(v[0]), Elem<T>::put(v[P - 1])};
+    uint16_t u[2];
+    memcpy(u, h, 4);
+    *reinterpret_cast<uint32_t*>(p) = u[0] | static_cast<uint32_t>(u[1]) << 16;
+  }
+}
+
+template <typename T, int P>
+__device__ __forceinline__ void weight_p(const void* w, int w_f32, int c, float (&v)[P]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] = 1.0f;
+  } else if (w_f32) {
+    load_p<float, P>(static_cast<const float*>(w) + c, v);
+  } else {
+    load_p<T, P>(static_cast<const T*>(w) + c, v);
+  }
+}
+
+// Rows without 16-byte alignment, up to 8 accesses a thread: like the kernel
+// above with P elements for a piece (piece i of thread t starts at column (i
+// blockDim.x + t) P, so that a warp's accesses lie side by side).
 constexpr int kNormElems = 8;
 
-template <typename T, bool Q8>
+template <typename T, int P, bool Q8>
 __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_elem_kernel(const NormArgs a) {
   constexpr int E = kNormElems;
   __shared__ float2 red[64];
@@ -416,67 +460,64 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_elem_kernel(const No
   pdl_trigger();
   if (row >= a.rows) return;  // (blocks of several rows have no barrier)
   const T* x = static_cast<const T*>(a.x) + row * a.xs;
-  float v[E];
+  float v[E][P];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const int c = i * blockDim.x + threadIdx.x;
-    v[i] = c < a.cols ? Elem<T>::get(x[c]) : 0.0f;
+    const int c = (i * blockDim.x + threadIdx.x) * P;
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[i][j] = 0.0f;
+    if (c < a.cols) load_p<T, P>(x + c, v[i]);
   }
   if (a.r != nullptr) {
     const T* r = static_cast<const T*>(a.r) + row * a.rs;
-    float rv[E];
+    float rv[E][P];
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = i * blockDim.x + threadIdx.x;
-      rv[i] = c < a.cols ? Elem<T>::get(r[c]) : 0.0f;
+      const int c = (i * blockDim.x + threadIdx.x) * P;
+#pragma unroll
+      for (int j = 0; j < P; ++j) rv[i][j] = 0.0f;
+      if (c < a.cols) load_p<T, P>(r + c, rv[i]);
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = i * blockDim.x + threadIdx.x;
-      const T sum = Elem<T>::put(v[i] + rv[i]);
-      v[i] = Elem<T>::get(sum);
-      if (c < a.cols && a.s != nullptr) static_cast<T*>(a.s)[row * a.ss + c] = sum;
-    }
-  }
-  float w[E];
-  if (a.w == nullptr) {
+      const int c = (i * blockDim.x + threadIdx.x) * P;
 #pragma unroll
-    for (int i = 0; i < E; ++i) w[i] = 1.0f;
-  } else if (a.w_f32) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * blockDim.x + threadIdx.x;
-      w[i] = c < a.cols ? static_cast<const float*>(a.w)[c] : 0.0f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int c = i * blockDim.x + threadIdx.x;
-      w[i] = c < a.cols ? Elem<T>::get(static_cast<const T*>(a.w)[c]) : 0.0f;
+      for (int j = 0; j < P; ++j) v[i][j] = Elem<T>::get(Elem<T>::put(v[i][j] + rv[i][j]));
+      if (c < a.cols && a.s != nullptr) store_p<T, P>(static_cast<T*>(a.s) + row * a.ss + c, v[i]);
     }
   }
   float ss = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) ss = fmaf(v[i], v[i], ss);
+  for (int i = 0; i < E; ++i)
+#pragma unroll
+    for (int j = 0; j < P; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   ss = row_sum2(ss, 0.0f, red, 0).x;
   float rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
   if (!mean_holds(ss / static_cast<float>(a.cols) + a.eps)) {
     const float p = norm_rescale(ss / static_cast<float>(a.cols) + a.eps);
     ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) ss = fmaf(v[i] * p, v[i] * p, ss);
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int j = 0; j < P; ++j) ss = fmaf(v[i][j] * p, v[i][j] * p, ss);
     ss = row_sum2(ss, 0.0f, red, 1).x;
     rstd = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps * p * p) * p;
   }
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const int c = i * blockDim.x + threadIdx.x;
-    v[i] = v[i] * rstd * w[i];
-    if (Q8) {
-      if (c < a.cols) m = max_abs(m, v[i]);
-    } else if (c < a.cols) {
-      static_cast<T*>(a.y)[row * a.ys + c] = Elem<T>::put(v[i]);
+    const int c = (i * blockDim.x + threadIdx.x) * P;
+    if (c < a.cols) {
+      float w[P];
+      weight_p<T, P>(a.w, a.w_f32, c, w);
+#pragma unroll
+      for (int j = 0; j < P; ++j) v[i][j] = v[i][j] * rstd * w[j];
+      if (Q8) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) m = max_abs(m, v[i][j]);
+      } else {
+        store_p<T, P>(static_cast<T*>(a.y) + row * a.ys + c, v[i]);
+      }
     }
   }
   if (Q8) {
@@ -485,10 +526,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_elem_kernel(const No
     if (threadIdx.x == 0) a.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const int c = i * blockDim.x + threadIdx.x;
-      if (c < a.cols)
-        static_cast<int8_t*>(a.y)[row * a.ys + c] =
-            f == 0.0f ? int8_t(0) : static_cast<int8_t>(q8_pack(v[i] * pre, 0.0f, 0.0f, 0.0f, f) & 0xFFu);
+      const int c = (i * blockDim.x + threadIdx.x) * P;
+      if (c < a.cols) {
+        const uint32_t q = f == 0.0f ? 0u : q8_pack(v[i][0] * pre, v[i][P - 1] * pre, 0.0f, 0.0f, f);
+        int8_t* y = static_cast<int8_t*>(a.y) + row * a.ys + c;
+        if (P == 1)
+          *y = static_cast<int8_t>(q & 0xFFu);
+        else
+          *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(q);
+      }
     }
   }
 }
@@ -769,11 +815,84 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   }
 }
 
+// Rows without 16-byte alignment, P elements an access, up to 8 a thread: dz
+// and the row statistic in one pass, a row a block (or a warp a row).
+constexpr int kNormBwdElemThreads = 512;
+
+template <typename T, int P>
+__global__ void __launch_bounds__(kNormBwdElemThreads) rms_norm_bwd_elem_kernel(const NormBwdArgs a) {
+  constexpr int E = kNormElems;
+  __shared__ float2 red[64];
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= a.rows) return;  // (blocks of several rows have no barrier)
+  const T* z = static_cast<const T*>(a.z) + row * a.zs;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.dys;
+  const T* ds = a.ds == nullptr ? nullptr : static_cast<const T*>(a.ds) + row * a.dss;
+  float zv[E][P], gw[E][P], d[E][P];
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * P;
+#pragma unroll
+    for (int j = 0; j < P; ++j) zv[i][j] = gw[i][j] = d[i][j] = 0.0f;
+    if (c < a.cols) {
+      load_p<T, P>(z + c, zv[i]);
+      load_p<T, P>(dy + c, gw[i]);
+      if (ds != nullptr) load_p<T, P>(ds + c, d[i]);  // (now, so that one latency covers all three)
+    }
+  }
+  float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * P;
+    if (c < a.cols) {
+      float w[P];
+      weight_p<T, P>(a.w, a.w_f32, c, w);
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        gw[i][j] *= w[j];
+        ss = fmaf(zv[i][j], zv[i][j], ss);
+        dot = fmaf(gw[i][j], zv[i][j], dot);
+      }
+    }
+  }
+  float2 t = row_sum2(ss, dot, red, 0);
+  const float ms = t.x / static_cast<float>(a.cols) + a.eps;
+  float rstd = __frsqrt_rn(ms);
+  float m = t.y * rstd / static_cast<float>(a.cols);
+  if (!mean_holds(ms)) {
+    const float p = norm_rescale(ms);
+    ss = dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        ss = fmaf(zv[i][j] * p, zv[i][j] * p, ss);
+        dot = fmaf(gw[i][j], zv[i][j] * p, dot);
+      }
+    t = row_sum2(ss, dot, red, 1);
+    const float r = __frsqrt_rn(t.x / static_cast<float>(a.cols) + a.eps * p * p);
+    m = t.y * r / static_cast<float>(a.cols);
+    rstd = r * p;
+  }
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    const int c = (i * blockDim.x + threadIdx.x) * P;
+    if (c < a.cols) {
+#pragma unroll
+      for (int j = 0; j < P; ++j) d[i][j] = fmaf(rstd, fmaf(-zv[i][j] * rstd, m, gw[i][j]), d[i][j]);
+      store_p<T, P>(static_cast<T*>(a.dz) + row * a.dzs + c, d[i]);
+    }
+  }
+}
+
 // Any width and alignment, one row a block at a time.  With dynamic shared
 // memory for a row of dw (`sums`) the block takes every gridDim.x-th row and
 // leaves a partial row of dw like the kernel above (each thread adds to its
 // own columns only); else it leaves the row statistic for
-// rms_norm_dw_loop_kernel.
+// rms_norm_dw_kernel.
 template <typename T>
 __global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArgs a, int sums) {
   extern __shared__ float sdw[];  // [cols] with sums
@@ -827,22 +946,30 @@ __global__ void __launch_bounds__(256) rms_norm_bwd_loop_kernel(const NormBwdArg
     for (int c = threadIdx.x; c < a.cols; c += 256) a.part[static_cast<long long>(blockIdx.x) * a.cols + c] = sdw[c];
 }
 
-// Partial sums of dw over the rows of one chunk: thread = column, block row
-// y = chunk.  Reads what the loop form's rows kernel left in rstd.
-template <typename T>
-__global__ void __launch_bounds__(128) rms_norm_dw_loop_kernel(const NormBwdArgs a, int chunk) {
+// Partial sums of dw over the rows of one chunk (blockIdx.y): a thread owns P
+// columns.  Reads what the rows' kernel left in rstd.
+template <typename T, int P>
+__global__ void __launch_bounds__(128) rms_norm_dw_kernel(const NormBwdArgs a, int chunk) {
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * 128 + threadIdx.x;
+  const long long c = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) * P;
   if (c >= a.cols) return;
   const long long r0 = static_cast<long long>(blockIdx.y) * chunk;
   const long long r1 = min(r0 + chunk, a.rows);
-  float v = 0.0f;
-#pragma unroll 4
-  for (long long r = r0; r < r1; ++r)
-    v = fmaf(Elem<T>::get(static_cast<const T*>(a.dy)[r * a.dys + c]),
-             Elem<T>::get(static_cast<const T*>(a.z)[r * a.zs + c]) * a.rstd[r], v);
-  a.part[static_cast<long long>(blockIdx.y) * a.cols + c] = v;
+  float v[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) v[j] = 0.0f;
+#pragma unroll 8
+  for (long long r = r0; r < r1; ++r) {
+    float g[P], z[P];
+    load_p<T, P>(static_cast<const T*>(a.dy) + r * a.dys + c, g);
+    load_p<T, P>(static_cast<const T*>(a.z) + r * a.zs + c, z);
+    const float rstd = a.rstd[r];
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] = fmaf(g[j], z[j] * rstd, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < P; ++j) a.part[static_cast<long long>(blockIdx.y) * a.cols + c + j] = v[j];
 }
 
 // dw[c] = sum of part[0..parts)[c], in a fixed order: 32 columns a block, 32
