@@ -450,7 +450,8 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
  * any size is taken; bases on 16-byte boundaries and strides of whole 16-byte
  * pieces run fastest (a product whose operands lack that first copies them
  * into the workspace, which is what its *_workspace_size query counts).
- * Row counts and widths are at most 2^30 (MSIGN_ERR_UNSUPPORTED beyond).
+ * Row counts and widths are at most 2^30, and a product has at most 2^29
+ * tiles of 256 x 128 outputs (MSIGN_ERR_UNSUPPORTED beyond).
  * An output at the address of another buffer of its call is refused
  * (MSIGN_ERR_INVALID_ARG) where the entry point does not allow it; other
  * overlaps are not looked for.

@@ -80,6 +80,10 @@ bool is_one_of(const void* p, std::initializer_list<const void*> others) {
   return false;
 }
 
+// Whether a product's 256 x 128 tiles can be counted in an int (the kernels'
+// tile numbers): looked at before anything is enqueued.
+bool countable(int64_t rows, int64_t cols) { return ceil_div(rows, 256) * ceil_div(cols, 128) <= INT32_MAX / 4; }
+
 // ---------------------------------------------------------------- RMS norm
 
 struct NormPlan {
@@ -542,7 +546,9 @@ msign_status ffn_check(msign_dtype dtype, int act, const FfnShape& s, int64_t x_
   if (!valid_dtype(dtype) || act < 0 || act > 2 || s.t < 0 || s.d < 0 || s.h < 0) return MSIGN_ERR_INVALID_ARG;
   if (!valid_stride(x_stride, s.d) || !valid_stride(w_stride, s.d)) return MSIGN_ERR_INVALID_ARG;
   if (dtype == MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
-  if (s.t > kMaxDim || s.d > kMaxDim || s.h > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  if (s.t > kMaxDim || s.d > kMaxDim || s.h > kMaxDim || !countable(s.t, s.h) || !countable(s.t, s.d) ||
+      !countable(s.h, s.d))
+    return MSIGN_ERR_UNSUPPORTED;
   return MSIGN_OK;
 }
 
@@ -671,7 +677,7 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
     return MSIGN_ERR_INVALID_ARG;
   if (m == 0 || n == 0) return MSIGN_OK;
   if (out == nullptr) return MSIGN_ERR_INVALID_ARG;
-  if (m > kMaxDim || n > kMaxDim || k > kMaxI8K) return MSIGN_ERR_UNSUPPORTED;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxI8K || !countable(m, n)) return MSIGN_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int odt = to_dt(out_dtype), oes = dtype_size(odt);
   const int64_t ldo = stride_of(out_stride, n);

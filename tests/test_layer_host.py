@@ -75,6 +75,7 @@ def test_i8_matmul_statuses(lib):
     for kw in (dict(a=None), dict(sa=None), dict(b=None), dict(sb=None), dict(out=None), dict(dt=5), dict(m=-1), dict(n=-1),
                dict(k=-1), dict(st=(63, 0, 0)), dict(st=(0, 63, 0)), dict(st=(0, 0, 63)), dict(st=(-64, 0, 0))):
         assert call(**kw) == BAD, kw
+    assert call(m=2 ** 30, n=2 ** 30, k=16) == UNS  # more tiles than the kernels count
     assert call(k=2 ** 17) == UNS and call(m=2 ** 30 + 1) == UNS and call(n=2 ** 30 + 1) == UNS
     assert call(k=65) == WS and call(k=65, ws=P, wsb=size(k=65) - 1) == WS and call(k=65, ws=P + 128, wsb=1 << 20) == WS
     assert call(m=0) == OK and call(n=0, out=None) == OK
@@ -91,7 +92,7 @@ def ffn_args(lib, **kw):
     (dict(x=None), BAD), (dict(wg=None), BAD), (dict(wu=None), BAD), (dict(out=None), BAD), (dict(g=P), BAD), (dict(u=P), BAD),
     (dict(dt=3), BAD), (dict(act=3), BAD), (dict(act=-1), BAD), (dict(t=-1), BAD), (dict(d=-1), BAD), (dict(h=-1), BAD),
     (dict(st=(63, 0, 0, 0)), BAD), (dict(st=(0, 63, 0, 0)), BAD), (dict(st=(0, 0, 63, 0)), BAD), (dict(st=(0, 0, 0, 63)), BAD),
-    (dict(dt=F), UNS), (dict(t=2 ** 30 + 1), UNS), (dict(d=2 ** 30 + 1), UNS), (dict(h=2 ** 30 + 1), UNS),
+    (dict(dt=F), UNS), (dict(t=2 ** 30 + 1), UNS), (dict(d=2 ** 30 + 1), UNS), (dict(h=2 ** 30 + 1), UNS), (dict(t=2 ** 30, h=2 ** 30), UNS),
     (dict(d=65), WS), (dict(x=P + 2), WS), (dict(wu=P + 8), WS),
     (dict(out=P), BAD), (dict(out=at(1)), BAD), (dict(g=at(3), u=at(4)), BAD), (dict(g=at(4), u=at(4)), BAD), (dict(st=(65, 0, 0, 0)), WS), (dict(st=(0, 68, 0, 0)), WS),
     (dict(t=0), OK), (dict(h=0, out=None), OK)])
