@@ -217,7 +217,7 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, int p
     int stages = std::min(kNormRing, kNormRingMax / per_sm / slot);
     while (stages < 2) stages = std::min(kNormRing, kNormRingMax / --per_sm / slot);
     parts = std::min<int64_t>({ceil_div(a.rows, y), int64_t(kPlanSms) * per_sm, kDwParts});  // what the workspace holds
-    const bool full = pieces == int64_t(x) * vpt;
+    const bool full = pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
     auto* k = vpt == 1   ? (full ? rms_norm_bwd_kernel<T, 1, true> : rms_norm_bwd_kernel<T, 1, false>)
               : vpt == 2 ? (full ? rms_norm_bwd_kernel<T, 2, true> : rms_norm_bwd_kernel<T, 2, false>)
               : vpt == 4 ? (full ? rms_norm_bwd_kernel<T, 4, true> : rms_norm_bwd_kernel<T, 4, false>)
@@ -253,7 +253,9 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, int p
     if (st != MSIGN_OK) return st;
   }
   if (dw == nullptr) return MSIGN_OK;
-  return launch(dw_reduce_kernel, dim3(static_cast<unsigned>(ceil_div(a.cols, 32))), dim3(32, 32), 0, 0, 3, 0.0,
+  const int quad = a.cols % 4 == 0 ? 4 : 1;
+  return launch(quad == 4 ? dw_reduce_kernel<4> : dw_reduce_kernel<1>,
+                dim3(static_cast<unsigned>(ceil_div(a.cols, 8 * quad))), dim3(256), 0, 0, 3, 0.0,
                 4.0 * parts * a.cols, stream, static_cast<const float*>(part), static_cast<int>(parts), a.cols, dw,
                 dw_dt);
 }

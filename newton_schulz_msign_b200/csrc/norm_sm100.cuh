@@ -142,6 +142,12 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   return r;
 }
 
+// The same value, as something that the compiler knows nothing of: it then
+// unpacks a piece again instead of holding the unpacked values in registers.
+__device__ __forceinline__ void opaque(uint4& u) {
+  asm volatile("" : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w));
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack2(const uint4& u, f32x2 (&v)[Elem<T>::vec / 2]) {
   float f[Elem<T>::vec];
@@ -625,20 +631,27 @@ __device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w,
 // dw_reduce_kernel (no atomics: the result does not depend on the order of
 // blocks).
 //
-// What bounds it: instructions and the latency of a row's join, at the 24
-// warps an SM that 80 registers a thread allow.  8192 x 4096 bf16 with ds 56
-// us, 4 of them dw_reduce_kernel; without the row's barrier 55, without dw
-// 50, without the second pass's arithmetic 50 (timing-only builds).  A warp a
-// row took 68, groups of warps with named barriers 51 to 54 but 2 to 4 more
-// on few rows, four blocks an SM 73 (spills).
+// FULL: every thread has a column and a row in every turn.
+//
+// What bounds it: 8192 x 4096 bf16 with ds 49 us, 41 of them HBM's; 3 are
+// dw_reduce_kernel, 1 the last turn of rows, the rest the first copies'
+// latency.  Before, it was instructions (31 a warp and 32 values, 56 us;
+// 27 now): threads that may be idle as branches, unpacked values held over
+// the barrier and spilled.  A running pointer to dz's row costs registers
+// (53), four blocks an SM spill (59), a warp a row leaves the instruction
+// caches (68).
 constexpr int kNormRing = 8;
 
 template <typename T, int VPT, bool FULL>
 __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1)
     rms_norm_bwd_kernel(const NormBwdArgs a, int stages) {
   constexpr int V = Elem<T>::vec, H = V / 2;
+  // The second pass unpacks z and dy again, from registers, or where a thread
+  // holds many pieces from shared memory (8192 x 8192 bf16 92 us from
+  // registers, 89 so; 4096 x 16384 107 and 103; at two pieces no difference).
+  constexpr bool kReread = VPT >= 4;
   extern __shared__ __align__(128) uint8_t ring[];  // [stages][z, dy, ds][blockDim.y][cols]
-  __shared__ float2 red[2][kNormBwdThreads / 32];
+  __shared__ __align__(16) float2 red[2][kNormBwdThreads / 32];
   __shared__ uint64_t full[kNormRing];
   const int lane = threadIdx.x & 31;
   const int ny = blockDim.y, nwarp = blockDim.x >> 5;       // rows of a group, warps of a row
@@ -692,17 +705,18 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     const bool mine = row < a.rows;
     ok = ok && wait_bounded(&full[st], phase, nullptr, a.err, a.timeout_ns);
     const uint8_t* src = ring + st * slot + threadIdx.y * row_bytes;
-    uint4 rz[VPT], ry[VPT];
+    uint4 rz[kReread ? 1 : VPT], ry[kReread ? 1 : VPT];
     f32x2 ss2 = 0, dot2 = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (mine && (FULL || c < a.cols)) {
+      if (FULL || (mine && c < a.cols)) {
         f32x2 zv[H], gv[H];
-        rz[i] = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
-        ry[i] = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
-        unpack2<T>(rz[i], zv);
-        unpack2<T>(ry[i], gv);
+        const uint4 uz = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
+        const uint4 uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
+        if (!kReread) rz[i] = uz, ry[i] = uy;
+        unpack2<T>(uz, zv);
+        unpack2<T>(uy, gv);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           ss2 = fma2(zv[j], zv[j], ss2);
@@ -723,8 +737,13 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
       const f32x2* r = reinterpret_cast<const f32x2*>(&red[par][warp0]);
       f32x2 t = r[0];
       if (nwarp == 8) {
+        f32x2 q[8];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) t = add2(t, r[i]);
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(r + 2 * i);
+          q[2 * i] = u.x, q[2 * i + 1] = u.y;
+        }
+        t = add2(add2(add2(q[0], q[1]), add2(q[2], q[3])), add2(add2(q[4], q[5]), add2(q[6], q[7])));
       } else {
         for (int i = 1; i < nwarp; ++i) t = add2(t, r[i]);
       }
@@ -732,7 +751,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     }
     float rstd = rsqrtf(fmaf(ss, inv, a.eps));
     float m = -dot * rstd * inv;  // minus the mean of dy w n
-    if (mine && !mean_holds(fmaf(ss, inv, a.eps))) {
+    if ((FULL || mine) && !mean_holds(fmaf(ss, inv, a.eps))) {
       // (the same for the whole row) each warp sums the row by itself: no
       // barrier that the block's other rows would have to meet
       const float p = norm_rescale(fmaf(ss, inv, a.eps));
@@ -746,10 +765,18 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (mine && (FULL || c < a.cols)) {
+      if (FULL || (mine && c < a.cols)) {
         f32x2 zv[H], gv[H], sv[H];
-        unpack2<T>(rz[i], zv);
-        unpack2<T>(ry[i], gv);
+        uint4 uz, uy;
+        if (kReread) {
+          uz = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
+          uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
+        } else {
+          uz = rz[i], uy = ry[i];
+          opaque(uz), opaque(uy);
+        }
+        unpack2<T>(uz, zv);
+        unpack2<T>(uy, gv);
         if (arrays == 3) {
           unpack2<T>(*reinterpret_cast<const uint4*>(src + 2 * ny * row_bytes + c * sizeof(T)), sv);
         } else {
@@ -972,32 +999,57 @@ __global__ void __launch_bounds__(128) rms_norm_dw_kernel(const NormBwdArgs a, i
   for (int j = 0; j < P; ++j) a.part[static_cast<long long>(blockIdx.y) * a.cols + c + j] = v[j];
 }
 
-// dw[c] = sum of part[0..parts)[c], in a fixed order: 32 columns a block, 32
-// threads a column take every 32nd partial, joined in shared memory.
-__global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* part, int parts, int cols, void* dw, int dt) {
-  __shared__ float sh[32][33];
+// dw[c] = sum of part[0..parts)[c], in a fixed order: 8 threads of P columns a
+// block, 32 threads a column take every 32nd partial, joined in shared memory.
+template <int P>
+struct DwPiece {
+  using type = float;
+};
+template <>
+struct DwPiece<4> {
+  using type = float4;
+};
+
+template <int P>
+__global__ void __launch_bounds__(256) dw_reduce_kernel(const float* part, int parts, int cols, void* dw, int dt) {
+  constexpr int kCols = 8 * P;
+  __shared__ float sh[32][kCols + 1];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * 32 + threadIdx.x;
-  float v = 0.0f;
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int c = blockIdx.x * kCols + tx * P;
+  float v[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) v[j] = 0.0f;
   if (c < cols) {
-    // sixteen loads at a time: the partials are few, and their latency is the kernel's time
-    for (int p0 = threadIdx.y; p0 < parts; p0 += 32 * 16) {
-      float t[16];
+    // sixteen loads at a time: the partials are few, and their latency is the
+    // kernel's time (rows past the last one are read as that one, so that no
+    // load waits for a branch)
+    for (int p0 = ty; p0 < parts; p0 += 32 * 16) {
+      typename DwPiece<P>::type t[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        t[i] = p0 + 32 * i < parts ? part[static_cast<long long>(p0 + 32 * i) * cols + c] : 0.0f;
+        t[i] = *reinterpret_cast<const typename DwPiece<P>::type*>(
+            part + static_cast<long long>(min(p0 + 32 * i, parts - 1)) * cols + c);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v += t[i];
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          if (p0 + 32 * i < parts) v[j] += reinterpret_cast<const float*>(&t[i])[j];
     }
   }
-  sh[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  v = sh[threadIdx.x][threadIdx.y];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  const int oc = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && oc < cols) store_elem(static_cast<char*>(dw) + static_cast<long long>(oc) * dtype_size(dt), dt, v);
+  for (int j = 0; j < P; ++j) sh[ty][tx * P + j] = v[j];
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    float r = sh[lane][warp * P + j];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    const int oc = blockIdx.x * kCols + warp * P + j;
+    if (lane == 0 && oc < cols) store_elem(static_cast<char*>(dw) + static_cast<long long>(oc) * dtype_size(dt), dt, r);
+  }
 }
 
 }  // namespace msb
