@@ -909,40 +909,74 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
   }
 }
 
+// P elements of a 16-bit type (8, 2 or 1) as one access.
+template <typename T, int P>
+__device__ __forceinline__ void load_n(const T* p, float* v) {
+  if constexpr (P == 8)
+    Elem<T>::unpack(*reinterpret_cast<const uint4*>(p), *reinterpret_cast<float(*)[8]>(v));
+  else
+    load_p<T, P>(p, *reinterpret_cast<float(*)[P]>(v));
+}
+
+template <typename T, int P>
+__device__ __forceinline__ void store_n(T* p, const float* v) {
+  if constexpr (P == 8)
+    *reinterpret_cast<uint4*>(p) = Elem<T>::pack(*reinterpret_cast<const float(*)[8]>(v));
+  else
+    store_p<T, P>(p, *reinterpret_cast<const float(*)[P]>(v));
+}
+
 // dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
 // rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
 // io type here, as the operands of the products that follow.
 //
-// 64 threads of a block take eight columns each, its four rows of threads
-// every (4 gridDim.y)-th row.  VEC: the inputs allow 16-byte loads; else they
-// are loaded one by one, and only the stores are wide.
-template <typename T, bool VEC>
+// 64 threads of a block take 512 columns, eight each, loaded by accesses of P
+// elements (what the rows' alignment allows: 8, 2 or 1); the block's four rows
+// of threads take every (4 gridDim.y)-th row.  Pairs are spread so that a
+// warp's accesses lie side by side, P = 2: 4096 x 2730 by pairs 7 us less than
+// one by one.  Single elements stay eight in a row, for the sake of a 16-byte
+// store (spread, 4096 x 2731 6 us more).
+template <typename T, int P>
 __global__ void __launch_bounds__(256) gated_dact_kernel(const T* dh, long long ldh, const T* gate, const T* up,
                                                          long long ldg, T* out, long long ldp, long long rows,
                                                          int cols, int act) {
+  constexpr int E = 8 / P;
+  constexpr int S = P == 2 ? 2 : 8;  // elements a store
   pdl_wait();
   pdl_trigger();
-  const long long c = (static_cast<long long>(blockIdx.x) * 64 + threadIdx.x) * 8;
-  if (c >= cols) return;
+  const long long c0 = static_cast<long long>(blockIdx.x) * 512 + threadIdx.x * S;
+  if (c0 >= ldp) return;
+  const int left = static_cast<int>(min(cols - c0, 512ll));  // columns from the thread's first one on
+  constexpr int kNext = P == 2 ? 64 * 2 : P;                 // from access to access
   const long long zs = rows * ldp;
   for (long long r = static_cast<long long>(blockIdx.y) * 4 + threadIdx.y; r < rows; r += 4ll * gridDim.y) {
+    const T *pd = dh + r * ldh + c0, *pg = gate + r * ldg + c0, *pu = up + r * ldg + c0;
     float d[8], g[8], u[8];
-    if (VEC) {
-      Elem<T>::unpack(*reinterpret_cast<const uint4*>(dh + r * ldh + c), d);
-      Elem<T>::unpack(*reinterpret_cast<const uint4*>(gate + r * ldg + c), g);
-      Elem<T>::unpack(*reinterpret_cast<const uint4*>(up + r * ldg + c), u);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool in = c + j < cols;
-        d[j] = in ? Elem<T>::get(dh[r * ldh + c + j]) : 0.0f;
-        g[j] = in ? Elem<T>::get(gate[r * ldg + c + j]) : 0.0f;
-        u[j] = in ? Elem<T>::get(up[r * ldg + c + j]) : 0.0f;
+    for (int i = 0; i < E; ++i) {
+      const bool in = i * kNext < left;  // (the padding: zeros)
+      if constexpr (P == 1) {
+        d[i] = in ? Elem<T>::get(pd[i]) : 0.0f;
+        g[i] = in ? Elem<T>::get(pg[i]) : 0.0f;
+        u[i] = in ? Elem<T>::get(pu[i]) : 0.0f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) d[i * P + j] = g[i * P + j] = u[i * P + j] = 0.0f;
+        if (in) {
+          load_n<T, P>(pd + i * kNext, d + i * P);
+          load_n<T, P>(pg + i * kNext, g + i * P);
+          load_n<T, P>(pu + i * kNext, u + i * P);
+        }
       }
     }
     gate_grad(d, g, u, act);
-    *reinterpret_cast<uint4*>(out + r * ldp + c) = Elem<T>::pack(g);
-    *reinterpret_cast<uint4*>(out + zs + r * ldp + c) = Elem<T>::pack(d);
+#pragma unroll
+    for (int i = 0; i < 8 / S; ++i) {
+      if (c0 + i * kNext < ldp) {
+        store_n<T, S>(out + r * ldp + c0 + i * kNext, g + i * S);
+        store_n<T, S>(out + zs + r * ldp + c0 + i * kNext, d + i * S);
+      }
+    }
   }
 }
 

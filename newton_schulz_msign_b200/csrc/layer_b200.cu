@@ -558,13 +558,18 @@ template <typename T>
 msign_status dact_run(const void* dh, int64_t ldh, const void* gate, const void* up, int64_t ldp_in, void* dgu,
                       const FfnShape& s, int act, cudaStream_t stream) {
   const int64_t ldp = round_up(s.h, 8);
-  const bool vec = s.h % 8 == 0 && rows_aligned(dh, ldh, s.t, 2) && rows_aligned(gate, ldp_in, s.t, 2) &&
-                   rows_aligned(up, ldp_in, s.t, 2);
+  // whether accesses of n elements reach every row
+  const auto reach = [&](int n) {
+    const auto in = [&](const void* p, int64_t ld) {
+      return reinterpret_cast<uintptr_t>(p) % (2 * n) == 0 && (s.t <= 1 || ld % n == 0);
+    };
+    return s.h % n == 0 && in(dh, ldh) && in(gate, ldp_in) && in(up, ldp_in);
+  };
   // about 16 blocks an SM, each a few rows
   const int64_t gx = ceil_div(ldp, 512);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(std::min<int64_t>(
                                                  ceil_div(s.t, 4), std::max<int64_t>(1, 16 * kPlanSms / gx))));
-  auto* k = vec ? gated_dact_kernel<T, true> : gated_dact_kernel<T, false>;
+  auto* k = reach(8) ? gated_dact_kernel<T, 8> : reach(2) ? gated_dact_kernel<T, 2> : gated_dact_kernel<T, 1>;
   return launch(k, grid, dim3(64, 4), 0, 0, 3, 0.0, 10.0 * s.t * s.h, stream, static_cast<const T*>(dh), ldh,
                 static_cast<const T*>(gate), static_cast<const T*>(up), ldp_in, static_cast<T*>(dgu), ldp, s.t,
                 static_cast<int>(s.h), act);
