@@ -433,10 +433,18 @@ bool stream_takes(int64_t rows, int64_t cols, int64_t z) {
 // between ranks, and 3 for every further generation of CTAs.  Measured against
 // single choices for all: tiles of at most 128 rows lose 22% on the 400 x 1000
 // x 2736 gated block (18.7 against 14.5 us), tiles of 256 rows 25% on 256 x
-// 4096 x 4096 int8 (15 against 11.8).
+// 4096 x 4096 int8 (15 against 11.8), two CTAs an SM for every narrow tile 12%
+// on 64 x 14336 x 4096 int8 (18.3 against 16.3), one wherever they fit 20% on
+// 16 x 4096 x 4096 int8 (5.4 against 4.5), and clusters counted as if they
+// filled all SMs 38% on dx of 1000 x 768 x 2048 (23.1 against 16.8).
 struct StreamPlan {
   int bn, splits, budget;
 };
+
+// CTAs that run at once as clusters of 1, 2, 4 and 8, one and two an SM (what
+// the occupancy query answers on a B200: clusters do not span the GPCs, and
+// some SMs of each are left over).
+constexpr int kClusterCtas[2][4] = {{148, 148, 132, 120}, {296, 296, 284, 264}};
 
 template <int MODE>
 StreamPlan stream_plan(int64_t rows, int64_t cols, int64_t z, int64_t steps) {
@@ -449,12 +457,18 @@ StreamPlan stream_plan(int64_t rows, int64_t cols, int64_t z, int64_t steps) {
     const int64_t bn = round_up(ceil_div(rows, ceil_div(rows, wide)), unit);  // equal tiles
     if (bn == tried) continue;
     tried = bn;
-    const int64_t per_sm = bn <= 128 ? 2 : 1;  // by shared memory
-    for (int splits = 1; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2) {
+    for (int splits = 1, log2 = 0; splits <= 8 && (splits == 1 || steps >= 2 * splits); splits *= 2, ++log2) {
       const int64_t ctas = tiles * ceil_div(rows, bn) * splits;
-      const int64_t gens = ceil_div(ctas, per_sm * kPlanSms);
       const double kb = ceil_div(steps, splits) * (128 + bn) * 128 / 1e3;  // loads of a CTA
-      const double busiest = static_cast<double>(per_sm == 1 ? gens : ceil_div(ctas, kPlanSms));
+      // CTAs an SM, by shared memory: narrow tiles two, unless one a SM are
+      // all of them and busy for long.  (Two of a long-lived cluster may share
+      // an SM while others are idle; short ones gain by overlapping the next
+      // launch.)
+      const bool fit = ctas <= kClusterCtas[0][log2], brief = kb < 320;
+      const int64_t per_sm = bn <= 128 && (!fit || brief) ? 2 : 1;
+      const int64_t gens = ceil_div(ctas, kClusterCtas[per_sm - 1][log2]);
+      const double busiest = static_cast<double>(
+          per_sm == 1 ? gens : std::max<int64_t>(fit || brief ? 1 : 2, ceil_div(ctas, kPlanSms)));
       const double mean = per_sm == 1 ? static_cast<double>(gens) : std::max(1.0, static_cast<double>(ctas) / kPlanSms);
       const double us = std::max(kb * busiest / 120, kb * mean / 100) + 0.02 * bn +
                         (splits > 1 ? 1.0 + 0.25 * splits : 0.0) +
