@@ -86,6 +86,47 @@ bool countable(int64_t rows, int64_t cols) { return ceil_div(rows, 256) * ceil_d
 
 // ---------------------------------------------------------------- RMS norm
 
+// How the norms' kernels reach the rows: by 16 bytes; by 16 bytes about the
+// boundaries that the rows are off (NORM_SHIFT's condition: one phase, and rows
+// of at least 32 pieces: gradients of 8192 x 151 bf16 13 us either way, 301 21
+// and 19, 1002 46 and 29); by `pair` elements.
+struct NormReach {
+  bool vec, shift;
+  int pair;
+};
+
+struct NormMatrix {
+  const void* p;
+  int64_t stride;
+  int es;
+};
+
+NormReach norm_reach(std::initializer_list<NormMatrix> ms, const void* weight, bool w_f32, int es, int64_t rows,
+                     int64_t cols) {
+  const int v = 16 / es;
+  // whether accesses of n elements reach every row of every matrix
+  const auto reach = [&](int n) {
+    // (a weight of fp32 is read 16 bytes at a time too)
+    const int ws = std::min(16, n * (w_f32 ? 4 : es));
+    if (cols % n != 0 || reinterpret_cast<uintptr_t>(weight) % ws != 0) return false;
+    for (const NormMatrix& m : ms)
+      if (m.p != nullptr &&
+          (reinterpret_cast<uintptr_t>(m.p) % (n * m.es) != 0 || (rows > 1 && m.stride % n != 0)))
+        return false;
+    return true;
+  };
+  const NormMatrix& first = *ms.begin();
+  bool shift = cols >= 32 * v;
+  for (const NormMatrix& m : ms) {
+    if (m.p == nullptr) continue;
+    const auto at = reinterpret_cast<uintptr_t>(m.p), to = reinterpret_cast<uintptr_t>(first.p);
+    shift = shift && at % m.es == 0 && at / m.es % v == to / first.es % v &&
+            (rows <= 1 || m.stride % v == first.stride % v);
+  }
+  const bool vec = reach(v);
+  return {vec, !vec && shift, reach(2) ? 2 : 1};
+}
+
 struct NormPlan {
   bool vec = false;
   int vpt = 0;
@@ -115,25 +156,31 @@ dim3 elem_block(int64_t cols, int pair) {
   return dim3(x, x == 32 ? 4 : 1);
 }
 
-// pair: the elements that one access may move where 16 bytes may not (1 or 2).
 template <typename T, bool Q8>
-msign_status norm_run(const NormArgs& a, bool vec_ok, int pair, double bytes, cudaStream_t stream) {
+msign_status norm_run(const NormArgs& a, const NormReach& by, double bytes, cudaStream_t stream) {
   NormPlan p;
-  if (vec_ok) p = norm_plan(a.cols / Elem<T>::vec);
+  if (by.vec) p = norm_plan(a.cols / Elem<T>::vec);
+  if (by.shift) p = norm_plan(norm_row_bytes(a.cols, sizeof(T), true) / 16);
   // Measured, the row in registers against the loop form, 8192 rows with a
   // residual: two elements an access, bf16, 1002 columns 23 and 31 us, 4098 93
   // and 109; fp32 4586 107 and 124; one element, bf16, 101 columns 6.7 and
   // 14.1, 2001 63 and 65, 4099 135 and 116.
-  if (!p.vec && a.cols <= pair * kNormElems * kNormMaxThreads && (pair == 2 || sizeof(T) == 4 || a.cols <= 2048)) {
-    const dim3 block = elem_block(a.cols, pair);
-    return launch(pair == 2 ? rms_norm_elem_kernel<T, 2, Q8> : rms_norm_elem_kernel<T, 1, Q8>,
+  if (!p.vec && a.cols <= by.pair * kNormElems * kNormMaxThreads &&
+      (by.pair == 2 || sizeof(T) == 4 || a.cols <= 2048)) {
+    const dim3 block = elem_block(a.cols, by.pair);
+    return launch(by.pair == 2 ? rms_norm_elem_kernel<T, 2, Q8> : rms_norm_elem_kernel<T, 1, Q8>,
                   dim3(static_cast<unsigned>(ceil_div(a.rows, block.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
   }
   if (!p.vec)
     return launch(rms_norm_loop_kernel<T, Q8>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
                   stream, a);
   const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, p.block.y)));
-  auto* k = p.vpt == 1 ? rms_norm_kernel<T, 1, Q8> : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8> : rms_norm_kernel<T, 4, Q8>;
+  auto* k = by.shift ? (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, true>
+                        : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, true>
+                                     : rms_norm_kernel<T, 4, Q8, true>)
+                     : (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, false>
+                        : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, false>
+                                     : rms_norm_kernel<T, 4, Q8, false>);
   return launch(k, grid, p.block, 0, 0, 3, 0.0, bytes, stream, a);
 }
 
@@ -163,27 +210,16 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
   a.ys = stride_of(y_stride, cols), a.ss = stride_of(s_stride, cols);
   a.rows = rows, a.cols = static_cast<int>(cols), a.eps = eps;
   a.w_f32 = w_dtype == MSIGN_FP32;
-  const int dt = to_dt(io_dtype), es = dtype_size(dt), v = 16 / es;
-  // whether accesses of n elements reach every row of every matrix
-  const auto reach = [&](int n) {
-    const auto in = [&](const void* p, int64_t stride, int size) {
-      return p == nullptr ||
-             (reinterpret_cast<uintptr_t>(p) % (n * size) == 0 && (rows <= 1 || stride % n == 0));
-    };
-    // (a weight of fp32 is read 16 bytes at a time too)
-    const int ws = std::min(16, n * (a.w_f32 ? 4 : es));
-    return cols % n == 0 && in(x, a.xs, es) && in(residual, a.rs, es) && in(sum_out, a.ss, es) &&
-           in(y, a.ys, q8 ? 1 : es) && reinterpret_cast<uintptr_t>(weight) % ws == 0;
-  };
-  const bool vec = reach(v);
-  const int pair = reach(2) ? 2 : 1;
+  const int dt = to_dt(io_dtype), es = dtype_size(dt);
+  const NormReach by = norm_reach({{x, a.xs, es}, {residual, a.rs, es}, {sum_out, a.ss, es}, {y, a.ys, q8 ? 1 : es}},
+                                  weight, a.w_f32, es, rows, cols);
   const double e = static_cast<double>(rows) * cols;
   const double bytes = e * es * (1 + (residual != nullptr) + (sum_out != nullptr)) + e * (q8 ? 1 : es);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dt == DT_BF16)
-    return q8 ? norm_run<__nv_bfloat16, true>(a, vec, pair, bytes, s) : norm_run<__nv_bfloat16, false>(a, vec, pair, bytes, s);
-  if (dt == DT_FP16) return q8 ? norm_run<__half, true>(a, vec, pair, bytes, s) : norm_run<__half, false>(a, vec, pair, bytes, s);
-  return q8 ? norm_run<float, true>(a, vec, pair, bytes, s) : norm_run<float, false>(a, vec, pair, bytes, s);
+    return q8 ? norm_run<__nv_bfloat16, true>(a, by, bytes, s) : norm_run<__nv_bfloat16, false>(a, by, bytes, s);
+  if (dt == DT_FP16) return q8 ? norm_run<__half, true>(a, by, bytes, s) : norm_run<__half, false>(a, by, bytes, s);
+  return q8 ? norm_run<float, true>(a, by, bytes, s) : norm_run<float, false>(a, by, bytes, s);
 }
 
 // Partial rows of dw that the gradients leave at most: four blocks an SM.
@@ -193,8 +229,16 @@ constexpr int64_t kLoopSums = 12000;   // columns whose sums it does (48 KB with
 constexpr int kSmemMax = 232448;       // shared memory of a block
 constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has some static shared memory too)
 
+template <typename T, int KIND>
+auto* norm_bwd_kernel(int vpt) {
+  return vpt == 1   ? rms_norm_bwd_kernel<T, 1, KIND>
+         : vpt == 2 ? rms_norm_bwd_kernel<T, 2, KIND>
+         : vpt == 4 ? rms_norm_bwd_kernel<T, 4, KIND>
+                    : rms_norm_bwd_kernel<T, 8, KIND>;
+}
+
 template <typename T>
-msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, int pair, char* ws, double bytes,
+msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, const NormReach& by, char* ws, double bytes,
                           cudaStream_t stream) {
   Carver cv(ws);
   float* part = static_cast<float*>(cv.take(sizeof(float) * std::min<int64_t>(a.rows, kDwParts) * a.cols));
@@ -202,32 +246,39 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, bool vec_ok, int p
   a.part = dw != nullptr ? part : nullptr;
   int64_t parts;
   msign_status st;
-  const int64_t pieces = a.cols / Elem<T>::vec;
-  const int row_bytes = a.cols * static_cast<int>(sizeof(T));
+  const int pair = by.pair;
+  const int row_bytes = static_cast<int>(norm_row_bytes(a.cols, sizeof(T), by.shift));
+  const int64_t pieces = row_bytes / 16;
   const int arrays = a.ds != nullptr ? 3 : 2;
-  if (vec_ok && pieces <= kNormBwdThreads * kNormBwdVpt) {
+  if ((by.vec || by.shift) && pieces <= kNormBwdThreads * kNormBwdVpt) {
     // as few pieces a thread as 256 threads a row allow, the block filled up
     // with rows, and the ring as deep as the SM's blocks leave room for
     int vpt = pieces <= 32 ? 1 : 2;
     while (pieces > vpt * kNormBwdThreads) vpt *= 2;
     const int x = static_cast<int>(round_up(ceil_div(pieces, vpt), 32));
     const int y = std::max(1, kNormBwdThreads / x);
-    int per_sm = vpt <= 2 ? 3 : vpt <= 4 ? 2 : 1;  // by the kernel's registers
+    // by the kernel's registers (80, 128 and 255 a thread)
+    int per_sm = std::min(4, (vpt <= 2 ? 3 : vpt <= 4 ? 2 : 1) * kNormBwdThreads / (x * y));
     const int slot = arrays * y * row_bytes;
-    int stages = std::min(kNormRing, kNormRingMax / per_sm / slot);
-    while (stages < 2) stages = std::min(kNormRing, kNormRingMax / --per_sm / slot);
+    // (an SM has 228 KB; each block 1 KB of its own and what the kernel declares)
+    const auto depth = [&] { return std::min(kNormRing, std::min(kNormRingMax, 228 * 1024 / per_sm - 1536) / slot); };
+    int stages = depth();
+    while (stages < 2) --per_sm, stages = depth();
     parts = std::min<int64_t>({ceil_div(a.rows, y), int64_t(kPlanSms) * per_sm, kDwParts});  // what the workspace holds
-    const bool full = pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
-    auto* k = vpt == 1   ? (full ? rms_norm_bwd_kernel<T, 1, true> : rms_norm_bwd_kernel<T, 1, false>)
-              : vpt == 2 ? (full ? rms_norm_bwd_kernel<T, 2, true> : rms_norm_bwd_kernel<T, 2, false>)
-              : vpt == 4 ? (full ? rms_norm_bwd_kernel<T, 4, true> : rms_norm_bwd_kernel<T, 4, false>)
-                         : (full ? rms_norm_bwd_kernel<T, 8, true> : rms_norm_bwd_kernel<T, 8, false>);
+    // a thread's rows have one phase: the rows from turn to turn are a multiple of a piece's elements apart
+    const int64_t period = std::max(1, Elem<T>::vec / y);
+    if (by.shift && parts * y < a.rows) parts = parts / period * period;
+    const bool full = by.vec && pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
+    auto* k = by.shift ? norm_bwd_kernel<T, NORM_SHIFT>(vpt)
+              : full   ? norm_bwd_kernel<T, NORM_FULL>(vpt)
+                       : norm_bwd_kernel<T, NORM_ROWS>(vpt);
     st = launch(k, dim3(static_cast<unsigned>(parts)), dim3(x, y), static_cast<size_t>(stages) * slot, 0, 3, 0.0,
                 bytes, stream, a, stages);
     if (st != MSIGN_OK) return st;
   } else if (dw != nullptr && a.cols <= kLoopSums && a.rows <= 2 * kDwParts) {
-    // few rows: one launch less (777 x 1001 fp32: 20 us a call with the host's
-    // part, 17 so; 16384 x 1001 129 us, and 93 with the sums of dw apart)
+    // few rows: one launch less (777 x 1001 fp32, phases apart: 20 us a call
+    // with the host's part, 17 so; 16384 x 1001 129 us, and 93 with the sums of
+    // dw apart)
     parts = std::min<int64_t>(a.rows, kDwParts);
     st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(parts)), dim3(256), sizeof(float) * a.cols, 0, 3,
                 0.0, bytes, stream, a, 1);
@@ -344,12 +395,9 @@ msign_status smem_limit(K kernel, int bytes) {
 
 template <typename T>
 msign_status norm_bwd_limits() {
-  for (msign_status st :
-       {smem_limit(rms_norm_bwd_kernel<T, 1, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 1, false>, kNormRingMax),
-        smem_limit(rms_norm_bwd_kernel<T, 2, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 2, false>, kNormRingMax),
-        smem_limit(rms_norm_bwd_kernel<T, 4, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 4, false>, kNormRingMax),
-        smem_limit(rms_norm_bwd_kernel<T, 8, true>, kNormRingMax), smem_limit(rms_norm_bwd_kernel<T, 8, false>, kNormRingMax)})
-    if (st != MSIGN_OK) return st;
+  for (int vpt : {1, 2, 4, 8})
+    for (auto* k : {norm_bwd_kernel<T, NORM_ROWS>(vpt), norm_bwd_kernel<T, NORM_FULL>(vpt), norm_bwd_kernel<T, NORM_SHIFT>(vpt)})
+      if (const msign_status st = smem_limit(k, kNormRingMax); st != MSIGN_OK) return st;
   return MSIGN_OK;
 }
 
@@ -644,7 +692,7 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   if (cols == 0) return MSIGN_OK;
   if (rows > kMaxDim || cols > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int dt = to_dt(io_dtype), es = dtype_size(dt), v = 16 / es;
+  const int dt = to_dt(io_dtype), es = dtype_size(dt);
   const int wdt = to_dt(w_dtype);
   if (rows == 0) return zero_rows(dw, cols, 1, cols, dtype_size(wdt), s);  // a sum over no rows
   if (dy == nullptr || sum == nullptr || dx == nullptr) return MSIGN_ERR_INVALID_ARG;
@@ -660,22 +708,13 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   a.dss = stride_of(dsum_stride, cols), a.dzs = stride_of(dx_stride, cols);
   a.rows = rows, a.cols = static_cast<int>(cols), a.w_f32 = w_dtype == MSIGN_FP32, a.eps = eps;
   a.err = dev->err, a.timeout_ns = kWaitLimitNs;
-  const auto reach = [&](int n) {  // (see norm_call)
-    const auto in = [&](const void* p, int64_t stride) {
-      return p == nullptr ||
-             (reinterpret_cast<uintptr_t>(p) % (n * es) == 0 && (rows <= 1 || stride % n == 0));
-    };
-    const int wsz = std::min(16, n * (a.w_f32 ? 4 : es));
-    return cols % n == 0 && in(dy, a.dys) && in(sum, a.zs) && in(dsum, a.dss) && in(dx, a.dzs) &&
-           reinterpret_cast<uintptr_t>(weight) % wsz == 0;
-  };
-  const bool vec = reach(v);
-  const int pair = reach(2) ? 2 : 1;
+  const NormReach by = norm_reach({{sum, a.zs, es}, {dy, a.dys, es}, {dsum, a.dss, es}, {dx, a.dzs, es}}, weight,
+                                  a.w_f32, es, rows, cols);
   const double bytes = static_cast<double>(rows) * cols * es * (3 + (dsum != nullptr));
   char* ws = dw != nullptr ? carve_base(workspace) : nullptr;
-  if (dt == DT_BF16) return norm_bwd_run<__nv_bfloat16>(a, dw, wdt, vec, pair, ws, bytes, s);
-  if (dt == DT_FP16) return norm_bwd_run<__half>(a, dw, wdt, vec, pair, ws, bytes, s);
-  return norm_bwd_run<float>(a, dw, wdt, vec, pair, ws, bytes, s);
+  if (dt == DT_BF16) return norm_bwd_run<__nv_bfloat16>(a, dw, wdt, by, ws, bytes, s);
+  if (dt == DT_FP16) return norm_bwd_run<__half>(a, dw, wdt, by, ws, bytes, s);
+  return norm_bwd_run<float>(a, dw, wdt, by, ws, bytes, s);
 }
 
 // ---------------------------------------------------------------- int8 product

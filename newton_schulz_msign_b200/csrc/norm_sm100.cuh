@@ -281,10 +281,85 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c, flo
   }
 }
 
+// Rows off 16-byte boundaries, by 16 bytes all the same: where every matrix of
+// the call has the same phase (the index of a row's first element past a
+// boundary, modulo the elements of 16 bytes), piece k of a row with phase ph
+// starts at column k vec - ph, and only its first and its last piece are not
+// whole (8192 rows with a residual, bf16: 1002 columns 17 us, by pairs 23;
+// 2001 33, one by one 61; 8191 137 and 224).
+template <typename T>
+__device__ __forceinline__ int row_phase(const void* p, long long at) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T) + static_cast<unsigned long long>(at)) %
+                          Elem<T>::vec);
+}
+
+template <typename T>
+__device__ __forceinline__ bool whole(int c, int cols) {
+  return c >= 0 && c + Elem<T>::vec <= cols;
+}
+
+// The piece at column c of a row, zeros outside the row.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ uint4 load_piece(const T* row, int c, int cols) {
+  if (SHIFT ? whole<T>(c, cols) : c < cols) return *reinterpret_cast<const uint4*>(row + c);
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (SHIFT && c < cols) {
+    float v[Elem<T>::vec];
+#pragma unroll
+    for (int j = 0; j < Elem<T>::vec; ++j)
+      v[j] = c + j >= 0 && c + j < cols ? Elem<T>::get(row[c + j]) : 0.0f;
+    u = Elem<T>::pack(v);
+  }
+  return u;
+}
+
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void store_piece(T* row, int c, int cols, const uint4& u) {
+  if (SHIFT ? whole<T>(c, cols) : c < cols) {
+    *reinterpret_cast<uint4*>(row + c) = u;
+  } else if (SHIFT && c < cols) {
+    float v[Elem<T>::vec];
+    Elem<T>::unpack(u, v);
+#pragma unroll
+    for (int j = 0; j < Elem<T>::vec; ++j)
+      if (c + j >= 0 && c + j < cols) row[c + j] = Elem<T>::put(v[j]);
+  }
+}
+
+// Elements of a piece outside the row become zeros (what was read there
+// belongs to the row's neighbours).
+template <typename T>
+__device__ __forceinline__ void keep_row(uint4& u, int c, int cols) {
+  float v[Elem<T>::vec];
+  Elem<T>::unpack(u, v);
+#pragma unroll
+  for (int j = 0; j < Elem<T>::vec; ++j)
+    if (c + j < 0 || c + j >= cols) v[j] = 0.0f;
+  u = Elem<T>::pack(v);
+}
+
+template <typename T>
+__device__ __forceinline__ float weight_at(const void* w, int w_f32, int c) {
+  if (w == nullptr) return 1.0f;
+  return w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::get(static_cast<const T*>(w)[c]);
+}
+
+// (One by one off the boundaries: cut out of the two 16-byte pieces about them
+// 8192 x 2001 takes as long, 8192 x 301 12 us instead of 10.6.)
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void load_weights(const void* w, int w_f32, int c, int cols, float (&v)[Elem<T>::vec]) {
+  if (!SHIFT) {
+    load_weight<T>(w, w_f32, c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < Elem<T>::vec; ++j) v[j] = c + j >= 0 && c + j < cols ? weight_at<T>(w, w_f32, c + j) : 0.0f;
+  }
+}
+
 // One row per blockDim.x threads (32: a warp a row, blockDim.y rows a block;
 // more: one row a block).  Piece i of thread t starts at column
 // (i blockDim.x + t) vec.
-template <typename T, int VPT, bool Q8>
+template <typename T, int VPT, bool Q8, bool SHIFT>
 __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArgs a) {
   constexpr int V = Elem<T>::vec;
   __shared__ float2 red[64];
@@ -294,11 +369,12 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
   pdl_trigger();
   if (row >= a.rows) return;  // (blocks of several rows have no barrier)
   const T* x = static_cast<const T*>(a.x) + row * a.xs;
+  const int ph = SHIFT ? row_phase<T>(a.x, row * a.xs) : 0;
   uint4 raw[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    raw[i] = c < a.cols ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
+    const int c = (i * blockDim.x + threadIdx.x) * V - ph;
+    raw[i] = load_piece<T, SHIFT>(x, c, a.cols);
   }
   if (a.r != nullptr) {
     const T* r = static_cast<const T*>(a.r) + row * a.rs;
@@ -306,19 +382,19 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
     uint4 rr[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      rr[i] = c < a.cols ? *reinterpret_cast<const uint4*>(r + c) : make_uint4(0, 0, 0, 0);
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
+      rr[i] = load_piece<T, SHIFT>(r, c, a.cols);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       float xv[V], rv[V];
       Elem<T>::unpack(raw[i], xv);
       Elem<T>::unpack(rr[i], rv);
 #pragma unroll
       for (int j = 0; j < V; ++j) xv[j] += rv[j];
       raw[i] = Elem<T>::pack(xv);  // the stored sum: what the norm and its gradient see
-      if (c < a.cols && a.s != nullptr) *reinterpret_cast<uint4*>(s + c) = raw[i];
+      if (a.s != nullptr) store_piece<T, SHIFT>(s, c, a.cols, raw[i]);
     }
   }
   float ss = 0.0f;
@@ -348,14 +424,14 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
     T* y = static_cast<T*>(a.y) + row * a.ys;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       if (c < a.cols) {
         float v[V], w[V];
         Elem<T>::unpack(raw[i], v);
-        load_weight<T>(a.w, a.w_f32, c, w);
+        load_weights<T, SHIFT>(a.w, a.w_f32, c, a.cols, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = v[j] * rstd * w[j];
-        *reinterpret_cast<uint4*>(y + c) = Elem<T>::pack(v);
+        store_piece<T, SHIFT>(y, c, a.cols, Elem<T>::pack(v));
       }
     }
   } else {
@@ -364,11 +440,11 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       Elem<T>::unpack(raw[i], v[i]);
       if (c < a.cols) {
         float w[V];
-        load_weight<T>(a.w, a.w_f32, c, w);
+        load_weights<T, SHIFT>(a.w, a.w_f32, c, a.cols, w);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           v[i][j] = v[i][j] * rstd * w[j];
@@ -387,25 +463,23 @@ __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_kernel(const NormArg
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       if (c < a.cols) {
         uint32_t p[V / 4];
 #pragma unroll
         for (int j = 0; j < V / 4; ++j)
           p[j] = f == 0.0f ? 0u : q8_pack(v[i][4 * j], v[i][4 * j + 1], v[i][4 * j + 2], v[i][4 * j + 3], f);
-        if (V == 8)
+        if (SHIFT && !whole<T>(c, a.cols)) {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (c + j >= 0 && c + j < a.cols) y[c + j] = static_cast<int8_t>(p[j / 4] >> (8 * (j % 4)) & 0xFFu);
+        } else if (V == 8)
           *reinterpret_cast<uint2*>(y + c) = make_uint2(p[0], p[V / 4 - 1]);
         else
           *reinterpret_cast<uint32_t*>(y + c) = p[0];
       }
     }
   }
-}
-
-template <typename T>
-__device__ __forceinline__ float weight_at(const void* w, int w_f32, int c) {
-  if (w == nullptr) return 1.0f;
-  return w_f32 ? static_cast<const float*>(w)[c] : Elem<T>::get(static_cast<const T*>(w)[c]);
 }
 
 // P consecutive elements (1 or 2), as floats.  Two move as one access, which
@@ -451,8 +525,8 @@ __device__ __forceinline__ void weight_p(const void* w, int w_f32, int c, float 
   }
 }
 
-// Rows without 16-byte alignment, up to 8 accesses a thread: like the kernel
-// above with P elements for a piece (piece i of thread t starts at column (i
+// Rows without 16-byte alignment whose phases differ or that are short, up to
+// 8 accesses a thread: like the kernel above with P elements for a piece (piece i of thread t starts at column (i
 // blockDim.x + t) P, so that a warp's accesses lie side by side).
 constexpr int kNormElems = 8;
 
@@ -631,7 +705,10 @@ __device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w,
 // dw_reduce_kernel (no atomics: the result does not depend on the order of
 // blocks).
 //
-// FULL: every thread has a column and a row in every turn.
+// NORM_FULL: every thread has a column and a row in every turn.  NORM_SHIFT:
+// rows off 16-byte boundaries, all matrices in the same phase (row_phase); a
+// thread's rows have one phase, so that its columns stay the same (16384 x 1001
+// bf16 with ds 44 us; by elements, dy and z read again for dw, 97).
 //
 // What bounds it: 8192 x 4096 bf16 with ds 49 us, 41 of them HBM's; 3 are
 // dw_reduce_kernel, 1 the last turn of rows, the rest the first copies'
@@ -641,29 +718,71 @@ __device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w,
 // (53), four blocks an SM spill (59), a warp a row leaves the instruction
 // caches (68).
 constexpr int kNormRing = 8;
+enum { NORM_ROWS, NORM_FULL, NORM_SHIFT };
 
-template <typename T, int VPT, bool FULL>
+// A row in shared memory: with SHIFT as it lies about its 16-byte boundaries.
+__host__ __device__ inline uint32_t norm_row_bytes(int cols, int es, bool shift) {
+  return shift ? (static_cast<uint32_t>(cols) * es + 31u - es) / 16u * 16u : static_cast<uint32_t>(cols) * es;
+}
+
+template <typename T, int VPT, int KIND>
 __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1)
     rms_norm_bwd_kernel(const NormBwdArgs a, int stages) {
   constexpr int V = Elem<T>::vec, H = V / 2;
+  constexpr bool FULL = KIND == NORM_FULL, SHIFT = KIND == NORM_SHIFT;
   // The second pass unpacks z and dy again, from registers, or where a thread
   // holds many pieces from shared memory (8192 x 8192 bf16 92 us from
   // registers, 89 so; 4096 x 16384 107 and 103; at two pieces no difference).
   constexpr bool kReread = VPT >= 4;
   extern __shared__ __align__(128) uint8_t ring[];  // [stages][z, dy, ds][blockDim.y][cols]
-  __shared__ __align__(16) float2 red[2][kNormBwdThreads / 32];
+  __shared__ __align__(16) float2 red[2][16];
   __shared__ uint64_t full[kNormRing];
   const int lane = threadIdx.x & 31;
   const int ny = blockDim.y, nwarp = blockDim.x >> 5;       // rows of a group, warps of a row
-  const int warp0 = threadIdx.y * nwarp;                    // this row's first warp
-  const int warp = warp0 + (threadIdx.x >> 5);
-  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  const int warp = threadIdx.y * nwarp + (threadIdx.x >> 5);
+  const int red0 = threadIdx.y * ((nwarp + 1) & ~1);        // where this row's warps leave their sums, in pairs
+  const uint32_t row_bytes = norm_row_bytes(a.cols, sizeof(T), SHIFT);
   const int arrays = a.ds != nullptr ? 3 : 2;
   const uint32_t slot = static_cast<uint32_t>(arrays * ny) * row_bytes;
   const long long step = static_cast<long long>(gridDim.x) * ny;
   // the group of rows from `row0` on into slot st, by the first warp: a copy a lane
   const auto fill = [&](long long row0, int st) {
     const int n = static_cast<int>(min(static_cast<long long>(ny), a.rows - row0));
+    if constexpr (SHIFT) {  // (24 copies at most)
+      const int arr = lane / n, y = lane - arr * n;
+      const bool mine = lane < arrays * n;
+      const long long row = row0 + y;
+      const T* src = static_cast<const T*>(arr == 0 ? a.z : arr == 1 ? a.dy : a.ds) +
+                     row * (arr == 0 ? a.zs : arr == 1 ? a.dys : a.dss);
+      uint8_t* dst = ring + st * slot + (arr * ny + y) * row_bytes;
+      uint32_t off = 0, bytes = 0;
+      if (mine) {
+        // whole 16-byte units, the neighbours' elements in the first and the
+        // last one too; but nothing before the matrix or behind it: what that
+        // cuts off comes element by element
+        const int ph = row_phase<T>(src, 0);
+        const int past = (ph + a.cols) % V;
+        int c0 = -ph, c1 = past == 0 ? a.cols : a.cols - past + V;
+        T* d = reinterpret_cast<T*>(dst) + ph;
+        if (row == 0 && ph != 0) {
+          c0 += V;
+          for (int c = 0; c < c0; ++c) d[c] = src[c];
+          fence_proxy_async_smem();  // (a later row's copy writes there)
+        }
+        if (row == a.rows - 1 && past != 0) {
+          c1 -= V;
+          for (int c = c1; c < a.cols; ++c) d[c] = src[c];
+        }
+        src += c0;
+        off = static_cast<uint32_t>(c0 + ph) * sizeof(T);
+        bytes = static_cast<uint32_t>(c1 - c0) * sizeof(T);
+      }
+      const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);  // (the elements are written, too)
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
+      __syncwarp();
+      if (mine) bulk_load(dst + off, src, bytes, &full[st]);
+      return;
+    }
     if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(arrays * n) * row_bytes);
     __syncwarp();
     for (int i = lane; i < arrays * n; i += 32) {
@@ -678,6 +797,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
   }
+  if (warp == 0) reinterpret_cast<float2*>(red)[lane] = make_float2(0.0f, 0.0f);  // (an odd row's last one stays so)
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -685,14 +805,16 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   if (warp == 0)
     for (int i = 0; i < stages; ++i)
       if (row0 + i * step < a.rows) fill(row0 + i * step, i);
+  // (the same in every turn: `step` is a multiple of the phases' period)
+  const int ph = SHIFT ? row_phase<T>(a.z, (row0 + threadIdx.y) * a.zs) : 0;
   f32x2 dw[VPT][H], w[VPT][H];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
+    const int c = (i * blockDim.x + threadIdx.x) * V - ph;
     float f[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] = 0.0f;
-    if (c < a.cols) load_weight<T>(a.w, a.w_f32, c, f);
+    if (c < a.cols) load_weights<T, SHIFT>(a.w, a.w_f32, c, a.cols, f);
 #pragma unroll
     for (int j = 0; j < H; ++j) dw[i][j] = 0, w[i][j] = pair2(f[2 * j], f[2 * j + 1]);
   }
@@ -709,11 +831,12 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     f32x2 ss2 = 0, dot2 = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       if (FULL || (mine && c < a.cols)) {
         f32x2 zv[H], gv[H];
-        const uint4 uz = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
-        const uint4 uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
+        uint4 uz = *reinterpret_cast<const uint4*>(src + (c + ph) * sizeof(T));
+        uint4 uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + (c + ph) * sizeof(T));
+        if (SHIFT && !whole<T>(c, a.cols)) keep_row<T>(uz, c, a.cols), keep_row<T>(uy, c, a.cols);
         if (!kReread) rz[i] = uz, ry[i] = uy;
         unpack2<T>(uz, zv);
         unpack2<T>(uy, gv);
@@ -729,24 +852,25 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     float v = (lane < 16 ? ss : dot) + __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? dot : ss, 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((lane & 15) == 0) reinterpret_cast<float*>(&red[par][warp])[lane >> 4] = v;
+    if ((lane & 15) == 0) reinterpret_cast<float*>(&red[par][red0 + (threadIdx.x >> 5)])[lane >> 4] = v;
     __syncthreads();
     // (past the barrier: the slot of the group before is free)
     if (warp == 0 && last >= 0 && row0 + (stages - 1) * step < a.rows) fill(row0 + (stages - 1) * step, last);
-    {  // every thread adds the row's warps up, in their order
-      const f32x2* r = reinterpret_cast<const f32x2*>(&red[par][warp0]);
-      f32x2 t = r[0];
+    {  // every thread adds the row's warps up, always in the same order
+      // (loads that do not wait for one another: 8192 x 2560 36 us, a loop 68)
+      const ulonglong2* r = reinterpret_cast<const ulonglong2*>(&red[par][red0]);
+      f32x2 q[4];
       if (nwarp == 8) {
-        f32x2 q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = add2(r[i].x, r[i].y);
+      } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(r + 2 * i);
-          q[2 * i] = u.x, q[2 * i + 1] = u.y;
+          q[i] = 0;
+          if (2 * i < nwarp) q[i] = add2(r[i].x, r[i].y);
         }
-        t = add2(add2(add2(q[0], q[1]), add2(q[2], q[3])), add2(add2(q[4], q[5]), add2(q[6], q[7])));
-      } else {
-        for (int i = 1; i < nwarp; ++i) t = add2(t, r[i]);
       }
+      const f32x2 t = add2(add2(q[0], q[1]), add2(q[2], q[3]));
       ss = unpair2(t).x, dot = unpair2(t).y;
     }
     float rstd = rsqrtf(fmaf(ss, inv, a.eps));
@@ -755,7 +879,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
       // (the same for the whole row) each warp sums the row by itself: no
       // barrier that the block's other rows would have to meet
       const float p = norm_rescale(fmaf(ss, inv, a.eps));
-      const float2 t = warp_sums<T>(reinterpret_cast<const T*>(src), reinterpret_cast<const T*>(src + ny * row_bytes),
+      const float2 t = warp_sums<T>(reinterpret_cast<const T*>(src) + ph,
+                                    reinterpret_cast<const T*>(src + ny * row_bytes) + ph,
                                     a.w, a.w_f32, a.cols, p);
       const float r = rsqrtf(fmaf(t.x, inv, a.eps * p * p));
       m = -t.y * r * inv;
@@ -764,13 +889,14 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     const f32x2 rstd2 = pair2(rstd, rstd), m2 = pair2(m, m);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
       if (FULL || (mine && c < a.cols)) {
         f32x2 zv[H], gv[H], sv[H];
         uint4 uz, uy;
         if (kReread) {
-          uz = *reinterpret_cast<const uint4*>(src + c * sizeof(T));
-          uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + c * sizeof(T));
+          uz = *reinterpret_cast<const uint4*>(src + (c + ph) * sizeof(T));
+          uy = *reinterpret_cast<const uint4*>(src + ny * row_bytes + (c + ph) * sizeof(T));
+          if (SHIFT && !whole<T>(c, a.cols)) keep_row<T>(uz, c, a.cols), keep_row<T>(uy, c, a.cols);
         } else {
           uz = rz[i], uy = ry[i];
           opaque(uz), opaque(uy);
@@ -778,7 +904,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
         unpack2<T>(uz, zv);
         unpack2<T>(uy, gv);
         if (arrays == 3) {
-          unpack2<T>(*reinterpret_cast<const uint4*>(src + 2 * ny * row_bytes + c * sizeof(T)), sv);
+          unpack2<T>(*reinterpret_cast<const uint4*>(src + 2 * ny * row_bytes + (c + ph) * sizeof(T)), sv);
         } else {
 #pragma unroll
           for (int j = 0; j < H; ++j) sv[j] = 0;
@@ -791,7 +917,11 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
           const float2 d = unpair2(fma2(rstd2, fma2(n, m2, mul2(gv[j], w[i][j])), sv[j]));
           o[2 * j] = d.x, o[2 * j + 1] = d.y;
         }
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + row * a.dzs + c) = Elem<T>::pack(o);
+        T* dz = static_cast<T*>(a.dz) + row * a.dzs;
+        if (SHIFT)
+          store_piece<T, SHIFT>(dz, c, a.cols, Elem<T>::pack(o));
+        else
+          *reinterpret_cast<uint4*>(dz + c) = Elem<T>::pack(o);
       }
     }
     last = st;
@@ -808,16 +938,25 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   }
   if (a.part == nullptr) return;
   float* out = a.part + static_cast<long long>(blockIdx.x) * a.cols;
+  const auto leave = [&](float* to, int c, const f32x2(&v)[H]) {
+#pragma unroll
+    for (int j = 0; j < H; j += 2) {
+      const float2 lo = unpair2(v[j]), hi = unpair2(v[j + 1]);
+      const float f[4] = {lo.x, lo.y, hi.x, hi.y};
+      if constexpr (SHIFT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c + 2 * j + k >= 0 && c + 2 * j + k < a.cols) to[c + 2 * j + k] = f[k];
+      } else {
+        *reinterpret_cast<float4*>(to + c + 2 * j) = make_float4(f[0], f[1], f[2], f[3]);
+      }
+    }
+  };
   if (ny == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c = (i * blockDim.x + threadIdx.x) * V;
-      if (c < a.cols)
-#pragma unroll
-        for (int j = 0; j < H; j += 2) {
-          const float2 lo = unpair2(dw[i][j]), hi = unpair2(dw[i][j + 1]);
-          *reinterpret_cast<float4*>(out + c + 2 * j) = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
+      const int c = (i * blockDim.x + threadIdx.x) * V - ph;
+      if (c < a.cols) leave(out, c, dw[i]);
     }
     return;
   }
@@ -826,13 +965,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (i * blockDim.x + threadIdx.x) * V;
-    if (c < a.cols)
-#pragma unroll
-      for (int j = 0; j < H; j += 2) {
-        const float2 lo = unpair2(dw[i][j]), hi = unpair2(dw[i][j + 1]);
-        *reinterpret_cast<float4*>(sdw + threadIdx.y * a.cols + c + 2 * j) = make_float4(lo.x, lo.y, hi.x, hi.y);
-      }
+    const int c = (i * blockDim.x + threadIdx.x) * V - ph;
+    if (c < a.cols) leave(sdw + threadIdx.y * a.cols, c, dw[i]);
   }
   __syncthreads();
   for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.cols; c += blockDim.x * ny) {
@@ -842,7 +976,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
   }
 }
 
-// Rows without 16-byte alignment, P elements an access, up to 8 a thread: dz
+// Rows without 16-byte alignment whose phases differ or that are short, P
+// elements an access, up to 8 a thread: dz
 // and the row statistic in one pass, a row a block (or a warp a row).
 constexpr int kNormBwdElemThreads = 512;
 

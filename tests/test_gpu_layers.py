@@ -206,6 +206,97 @@ def test_rms_norm_backward_against_differences():
     assert abs(float((dw.double() * vw.double()).sum()) - d) <= 1e-5 * float((dw.double() * vw.double()).abs().sum())
 
 
+def inside(t, lead, pad, tail, fill):
+    """The same values as rows ``pad`` elements apart, ``lead`` elements into a larger buffer of ``fill`` that goes on
+    for ``tail`` elements behind the last row; and that buffer."""
+    rows, cols = t.shape
+    big = torch.full((lead + rows * (cols + pad) - pad + tail,), fill, device="cuda").to(t.dtype)
+    v = big.as_strided((rows, cols), (cols + pad, 1), lead)
+    v.copy_(t)
+    return v, big
+
+
+def untouched(v, big, fill):
+    """Whether the buffer around a view from ``inside`` still holds its fill."""
+    around = torch.ones_like(big, dtype=torch.bool)
+    around.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(False)
+    return bool((big[around] == fill).all())
+
+
+# Rows off 16-byte boundaries: every matrix in the same phase (x_lead = lead), with rows that start in all phases or in
+# one, first and last rows whose neighbours belong to nobody; and one matrix apart from the others.
+OFF = [(0, 0, 0), (1, 0, 1), (3, 0, 0), (5, 1, 0), (7, 2, 3), (2, 5, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("rows,cols", [(1, 257), (41, 257), (19, 1001), (600, 1003), (5, 2046), (7, 4099), (3, 16383), (2, 20001)])
+@pytest.mark.parametrize("lead,pad,apart", OFF)
+def test_rms_norm_off_boundaries(dtype, rows, cols, lead, pad, apart):
+    nan = float("nan")
+    x, _ = inside(randn((rows, cols), 40, dtype), lead + apart, pad, 0, nan)
+    r, _ = inside(randn((rows, cols), 41, dtype), lead, pad, 0, nan)
+    w = randn((cols,), 42, dtype if rows % 2 else FP32)
+    y, yb = inside(torch.zeros_like(x), lead, pad, 40, 3)
+    s, sb = inside(torch.zeros_like(x), lead, pad, 40, 3)
+    msb.rms_norm(x, w, r, eps=1e-5, out=y, sum_out=s)
+    q, qb = inside(torch.zeros((rows, cols), dtype=torch.int8, device="cuda"), lead, pad, 40, 3)
+    _, scale, s8 = msb.rms_norm_q8(x, w, r, eps=1e-5, out=q)
+    msb.sync_status()
+    want_s = (x.float() + r.float()).to(dtype)
+    assert torch.equal(s, want_s) and torch.equal(s8, want_s)
+    want = L.rms(want_s, w, 1e-5)
+    # (the bounds of test_rms_norm and test_rms_norm_q8)
+    assert L.worst(y, want, want.abs() * (L.U[dtype] + 100 * 2.0 ** -24) + L.TINY[dtype]) <= 1
+    amax, rel = want.abs().amax(1), 110 * 2.0 ** -24
+    assert L.worst(scale, amax / 127, amax / 127 * rel) <= 1
+    assert L.worst(q, want / (amax / 127)[:, None], torch.tensor(0.5 + 127 * 2 * rel, device="cuda")) <= 1
+    assert untouched(y, yb, 3) and untouched(s, sb, 3) and untouched(q, qb, 3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("rows,cols", [(1, 257), (41, 257), (19, 1001), (2500, 1003), (5, 2046), (7, 4099), (700, 4607),
+                                       (3, 16381), (2, 20001)])
+@pytest.mark.parametrize("lead,pad,apart", OFF)
+def test_rms_norm_backward_off_boundaries(dtype, rows, cols, lead, pad, apart):
+    nan = float("nan")
+    s, _ = inside(randn((rows, cols), 43, dtype), lead, pad, 0, nan)
+    dy, _ = inside(randn((rows, cols), 44, dtype), lead + apart, pad, 0, nan)
+    ds = inside(randn((rows, cols), 45, dtype), lead, pad, 0, nan)[0] if rows % 2 else None
+    w = randn((cols,), 46, dtype if rows % 2 else FP32)
+    dx, xb = inside(torch.zeros_like(s), lead, pad, 40, 3)
+    _, dw = msb.rms_norm_backward(dy, s, w, dsum=ds, eps=1e-5, dx_out=dx)
+    msb.sync_status()
+    wx, ww, mx, mw = L.rms_backward(dy, s, w, ds, 1e-5)
+    serial = 200 + math.ceil(rows / 100)  # (see test_rms_norm_backward)
+    assert L.worst(dx, wx, wx.abs() * L.U[dtype] + mx * serial * 2.0 ** -24 + L.TINY[dtype]) <= 1
+    assert L.worst(dw, ww, ww.abs() * L.U[w.dtype] + mw * serial * 2.0 ** -24 + L.TINY[w.dtype]) <= 1
+    assert untouched(dx, xb, 3)
+    again = msb.rms_norm_backward(dy, s, w, dsum=ds, eps=1e-5)
+    assert torch.equal(again[1], dw) or apart or lead or pad  # (rows elsewhere may lie in other blocks)
+
+
+def test_rms_norm_off_boundaries_at_the_ends_of_the_range():
+    # squares beyond fp32, an infinity and a NaN, in rows whose neighbours share their 16 bytes
+    x = randn((24, 1001), 47, FP32)
+    x[3] *= 1e25
+    x[8] *= 1e-25
+    x[11, 1000] = float("inf")
+    x[14, 0] = float("nan")
+    x[20] = 0.0
+    dy = randn((24, 1001), 48, FP32)
+    y = msb.rms_norm(x, eps=0.0)
+    dx, _ = msb.rms_norm_backward(dy, x, eps=0.0)
+    msb.sync_status()
+    ok = [i for i in range(24) if i not in (11, 14, 20)]
+    want = L.rms(x, None, 0.0)[ok]
+    assert L.worst(y[ok], want, want.abs() * (L.U[FP32] + 100 * 2.0 ** -24) + L.TINY[FP32]) <= 1
+    wx, _, mx, _ = L.rms_backward(dy, x, None, None, 0.0)
+    assert L.worst(dx[ok], wx[ok], wx[ok].abs() * L.U[FP32] + mx[ok] * 201 * 2.0 ** -24 + L.TINY[FP32]) <= 1
+    for i in (11, 14, 20):
+        assert not bool(torch.isfinite(y[i]).all())
+    assert bool(torch.isnan(dx[14]).all()) and bool(torch.isnan(dx[20]).all())
+
+
 # ---------------------------------------------------------------- i8_matmul
 
 def i8(shape, seed):
