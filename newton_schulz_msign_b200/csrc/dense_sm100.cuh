@@ -872,40 +872,73 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
 
 // ---------------------------------------------------------------- around the products
 
-// Rows of `cols` elements copied to rows of ld_out elements (a 16-byte
-// multiple), the rest zero: what a tensor map needs where the caller's rows
-// do not start on 16-byte boundaries.  One launch for up to three matrices
-// (blockIdx.y).  U: the element as a whole number.  HBM-bound; the loads are
-// single elements, side by side across a warp.
+// Rows copied to rows of whole 16-byte pieces, the rest of the last one zero:
+// what a tensor map needs where the caller's rows do not start on 16-byte
+// boundaries.  One launch for up to three matrices (blockIdx.y).  Sizes in
+// bytes.  HBM-bound: a piece is cut out of the two aligned ones about it, except
+// where one of them reaches out of the matrix (4096 x 14335 int8 20 us, by
+// single elements 38; two of 14336 x 4095 bf16 84 and 98).  One piece a thread
+// and turn at full occupancy; four of them at once 24 and 102.
 struct PadArgs {
-  const void* in[3];
-  void* out[3];
-  long long ld_in[3], ld_out[3], rows[3];
-  int cols[3];
+  const uint8_t* in[3];
+  uint8_t* out[3];
+  long long ld[3], rows[3], bytes[3];  // from row to row of the input; rows; bytes of one
 };
 
-template <typename U>
-__global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
+// The 16 bytes at p of which the first n are the row's (the others become
+// zeros), in a matrix from `first` to `end`.
+__device__ __forceinline__ uint4 cut_piece(const uint8_t* p, int n, const uint8_t* first, const uint8_t* end) {
+  const int by = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint8_t* at = p - by;
+  const bool two = by + n > 16;
+  uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (at >= first && at + (two ? 32 : 16) <= end) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(at);
+    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+    if (two) {
+      const uint4 hi = *reinterpret_cast<const uint4*>(at + 16);
+      w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+    }
+    if (by & 8) {
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (by & 4) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (by & 3));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = n - 4 * i;  // of word i
+    w[i] = left >= 4 ? w[i] : left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ PadArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = 16 / sizeof(U);
   const int m = blockIdx.y;
-  const U* in = static_cast<const U*>(a.in[m]);
-  U* out = static_cast<U*>(a.out[m]);
-  const long long ld_in = a.ld_in[m], ld_out = a.ld_out[m], per = ld_out / V;
-  const int cols = a.cols[m];
-  const long long total = a.rows[m] * per;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < total; i += 256ll * gridDim.x) {
-    const long long r = i / per;
-    const int c = static_cast<int>(i - r * per) * V;
-    union {
-      uint4 v;
-      U e[V];
-    } o;
-    const U* src = in + r * ld_in + c;
-#pragma unroll
-    for (int j = 0; j < V; ++j) o.e[j] = c + j < cols ? src[j] : U(0);
-    *reinterpret_cast<uint4*>(out + r * ld_out + c) = o.v;
+  const uint8_t* in = a.in[m];
+  const long long ld = a.ld[m], rows = a.rows[m], bytes = a.bytes[m], per = (bytes + 15) / 16;
+  const uint8_t* end = in + (rows - 1) * ld + bytes;
+  // piece j of row r, and from turn to turn (the grid's threads and a row's
+  // pieces are counted in 32 bits)
+  const uint32_t first = blockIdx.x * 256u + threadIdx.x, step = 256u * gridDim.x, p32 = static_cast<uint32_t>(per);
+  long long r = first / p32, j = first % p32;
+  const uint32_t step_r = step / p32, step_j = step % p32;
+  while (r < rows) {
+    *reinterpret_cast<uint4*>(a.out[m] + (r * per + j) * 16) =
+        cut_piece(in + r * ld + j * 16, static_cast<int>(min(bytes - j * 16, 16ll)), in, end);
+    r += step_r, j += step_j;
+    if (j >= per) j -= per, ++r;
   }
 }
 

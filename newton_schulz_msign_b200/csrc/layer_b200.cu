@@ -355,26 +355,24 @@ void carve_operand(Carver& cv, const Operand& o, void** copy) { *copy = o.direct
 msign_status place_operands(std::initializer_list<Operand*> ops, std::initializer_list<void*> copies,
                             cudaStream_t stream) {
   PadArgs a = {};
-  int n = 0, es = 0;
+  int n = 0;
   int64_t most = 0;
   double bytes = 0.0;
   auto copy = copies.begin();
   for (Operand* o : ops) {
     void* to = *copy++;
     if (to == nullptr) continue;
-    es = o->es;
-    a.in[n] = o->p, a.ld_in[n] = o->ld, a.out[n] = to, a.ld_out[n] = o->padded_ld();
-    a.rows[n] = o->rows, a.cols[n] = static_cast<int>(o->cols);
-    most = std::max(most, o->rows * (o->padded_ld() * es / 16));
-    bytes += 2.0 * o->rows * o->cols * es;
+    a.in[n] = static_cast<const uint8_t*>(o->p), a.out[n] = static_cast<uint8_t*>(to);
+    a.ld[n] = o->ld * o->es, a.rows[n] = o->rows, a.bytes[n] = o->cols * o->es;
+    most = std::max(most, o->rows * (o->padded_ld() * o->es / 16));
+    bytes += 2.0 * o->rows * o->cols * o->es;
     o->p = to;
     o->ld = o->padded_ld();
     ++n;
   }
   if (n == 0) return MSIGN_OK;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ceil_div(most, 256), 16 * kPlanSms)), static_cast<unsigned>(n));
-  return launch(es == 1 ? pad_rows_kernel<uint8_t> : pad_rows_kernel<uint16_t>, grid, dim3(256), 0, 0, 2, 0.0, bytes,
-                stream, a);
+  return launch(pad_rows_kernel, grid, dim3(256), 0, 0, 2, 0.0, bytes, stream, a);
 }
 
 // Instruction descriptor: D type (fp32 or int32), A and B types, which of
