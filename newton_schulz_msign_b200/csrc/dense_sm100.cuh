@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
 
 // ---------------------------------------------------------------- around the products
 
-// Rows copied to rows of whole 16-byte pieces, the rest of the last one zero:
+// Rows copied as whole 16-byte pieces, the rest of the last one zero:
 // what a tensor map needs where the caller's rows do not start on 16-byte
 // boundaries.  One launch for up to three matrices (blockIdx.y).  Sizes in
 // bytes.  HBM-bound: a piece is cut out of the two aligned ones about it, except
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) dense_stream_kernel(const _
 struct PadArgs {
   const uint8_t* in[3];
   uint8_t* out[3];
-  long long ld[3], rows[3], bytes[3];  // from row to row of the input; rows; bytes of one
+  long long ld[3], ld_out[3], rows[3], bytes[3];  // from row to row; rows; bytes of one
 };
 
 // The 16 bytes at p of which the first n are the row's (the others become
@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
   pdl_trigger();
   const int m = blockIdx.y;
   const uint8_t* in = a.in[m];
-  const long long ld = a.ld[m], rows = a.rows[m], bytes = a.bytes[m], per = (bytes + 15) / 16;
+  const long long ld = a.ld[m], ld_out = a.ld_out[m], rows = a.rows[m], bytes = a.bytes[m], per = (bytes + 15) / 16;
   const uint8_t* end = in + (rows - 1) * ld + bytes;
   // piece j of row r, and from turn to turn (the grid's threads and a row's
   // pieces are counted in 32 bits)
@@ -935,7 +935,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const __grid_constant__ P
   long long r = first / p32, j = first % p32;
   const uint32_t step_r = step / p32, step_j = step % p32;
   while (r < rows) {
-    *reinterpret_cast<uint4*>(a.out[m] + (r * per + j) * 16) =
+    *reinterpret_cast<uint4*>(a.out[m] + r * ld_out + j * 16) =
         cut_piece(in + r * ld + j * 16, static_cast<int>(min(bytes - j * 16, 16ll)), in, end);
     r += step_r, j += step_j;
     if (j >= per) j -= per, ++r;
@@ -960,7 +960,7 @@ __device__ __forceinline__ void store_n(T* p, const float* v) {
 }
 
 // dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
-// rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
+// rows of ldp elements (a multiple of 64).  HBM-bound; both are rounded to the
 // io type here, as the operands of the products that follow.
 //
 // 64 threads of a block take 512 columns, eight each, loaded by accesses of P
