@@ -233,8 +233,7 @@ template <typename T, int KIND>
 auto* norm_bwd_kernel(int vpt) {
   return vpt == 1   ? rms_norm_bwd_kernel<T, 1, KIND>
          : vpt == 2 ? rms_norm_bwd_kernel<T, 2, KIND>
-         : vpt == 4 ? rms_norm_bwd_kernel<T, 4, KIND>
-                    : rms_norm_bwd_kernel<T, 8, KIND>;
+                    : rms_norm_bwd_kernel<T, 4, KIND>;
 }
 
 template <typename T>
@@ -250,15 +249,18 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, const NormReach& b
   const int row_bytes = static_cast<int>(norm_row_bytes(a.cols, sizeof(T), by.shift));
   const int64_t pieces = row_bytes / 16;
   const int arrays = a.ds != nullptr ? 3 : 2;
-  if ((by.vec || by.shift) && pieces <= kNormBwdThreads * kNormBwdVpt) {
-    // as few pieces a thread as 256 threads a row allow, the block filled up
-    // with rows, and the ring as deep as the SM's blocks leave room for
+  if ((by.vec || by.shift) && pieces <= norm_bwd_threads(kNormBwdVpt) * kNormBwdVpt) {
+    // one or two pieces a thread as far as 256 threads a row hold it, then four
+    // (up to 512 threads: 2048 x 16001 bf16 74 us, eight pieces 81; 4096 x 4700
+    // fp32 51 and 66; 8192 x 10240 bf16 129 and 123), the block filled up with
+    // rows, and the ring as deep as the SM's blocks leave room for
     int vpt = pieces <= 32 ? 1 : 2;
-    while (pieces > vpt * kNormBwdThreads) vpt *= 2;
+    if (pieces > vpt * norm_bwd_threads(vpt)) vpt = kNormBwdVpt;
     const int x = static_cast<int>(round_up(ceil_div(pieces, vpt), 32));
-    const int y = std::max(1, kNormBwdThreads / x);
-    // by the kernel's registers (80, 128 and 255 a thread)
-    int per_sm = std::min(4, (vpt <= 2 ? 3 : vpt <= 4 ? 2 : 1) * kNormBwdThreads / (x * y));
+    const int y = std::max(1, 256 / x);
+    const bool full = by.vec && pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
+    // by the kernel's registers (80 a thread; with four pieces 128, fp32 with idle threads 112)
+    int per_sm = std::min(4, (vpt <= 2 ? 768 : sizeof(T) == 4 && !full ? 576 : 512) / (x * y));
     const int slot = arrays * y * row_bytes;
     // (an SM has 228 KB; each block 1 KB of its own and what the kernel declares)
     const auto depth = [&] { return std::min(kNormRing, std::min(kNormRingMax, 228 * 1024 / per_sm - 1536) / slot); };
@@ -268,7 +270,6 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, const NormReach& b
     // a thread's rows have one phase: the rows from turn to turn are a multiple of a piece's elements apart
     const int64_t period = std::max(1, Elem<T>::vec / y);
     if (by.shift && parts * y < a.rows) parts = parts / period * period;
-    const bool full = by.vec && pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
     auto* k = by.shift ? norm_bwd_kernel<T, NORM_SHIFT>(vpt)
               : full   ? norm_bwd_kernel<T, NORM_FULL>(vpt)
                        : norm_bwd_kernel<T, NORM_ROWS>(vpt);
@@ -399,7 +400,7 @@ msign_status smem_limit(K kernel, int bytes) {
 
 template <typename T>
 msign_status norm_bwd_limits() {
-  for (int vpt : {1, 2, 4, 8})
+  for (int vpt : {1, 2, 4})
     for (auto* k : {norm_bwd_kernel<T, NORM_ROWS>(vpt), norm_bwd_kernel<T, NORM_FULL>(vpt), norm_bwd_kernel<T, NORM_SHIFT>(vpt)})
       if (const msign_status st = smem_limit(k, kNormRingMax); st != MSIGN_OK) return st;
   return MSIGN_OK;

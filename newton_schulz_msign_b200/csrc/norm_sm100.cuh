@@ -157,8 +157,10 @@ __device__ __forceinline__ void unpack2(const uint4& u, f32x2 (&v)[Elem<T>::vec 
 }
 
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBwdThreads = 256;  // largest block of the gradients' kernel
-constexpr int kNormBwdVpt = 8;        // and pieces of a row that one of its threads holds at most
+// Largest block of the gradients' kernel, by the pieces of a row that a thread
+// holds.
+__host__ __device__ constexpr int norm_bwd_threads(int vpt) { return vpt <= 2 ? 256 : 512; }
+constexpr int kNormBwdVpt = 4;  // and these at most
 constexpr int kNormVpt = 4;  // 16-byte pieces of a row that one thread holds at most
 
 struct NormArgs {
@@ -726,7 +728,7 @@ __host__ __device__ inline uint32_t norm_row_bytes(int cols, int es, bool shift)
 }
 
 template <typename T, int VPT, int KIND>
-__global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 : 1)
+__global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
     rms_norm_bwd_kernel(const NormBwdArgs a, int stages) {
   constexpr int V = Elem<T>::vec, H = V / 2;
   constexpr bool FULL = KIND == NORM_FULL, SHIFT = KIND == NORM_SHIFT;
@@ -859,18 +861,23 @@ __global__ void __launch_bounds__(kNormBwdThreads, VPT <= 2 ? 3 : VPT <= 4 ? 2 :
     {  // every thread adds the row's warps up, always in the same order
       // (loads that do not wait for one another: 8192 x 2560 36 us, a loop 68)
       const ulonglong2* r = reinterpret_cast<const ulonglong2*>(&red[par][red0]);
-      f32x2 q[4];
-      if (nwarp == 8) {
+      constexpr int Q = norm_bwd_threads(VPT) / 64;
+      f32x2 q[Q];
+      if (nwarp == 2 * Q) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = add2(r[i].x, r[i].y);
+        for (int i = 0; i < Q; ++i) q[i] = add2(r[i].x, r[i].y);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < Q; ++i) {
           q[i] = 0;
           if (2 * i < nwarp) q[i] = add2(r[i].x, r[i].y);
         }
       }
-      const f32x2 t = add2(add2(q[0], q[1]), add2(q[2], q[3]));
+#pragma unroll
+      for (int o = Q / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) q[i] = add2(q[2 * i], q[2 * i + 1]);
+      const f32x2 t = q[0];
       ss = unpair2(t).x, dot = unpair2(t).y;
     }
     float rstd = rsqrtf(fmaf(ss, inv, a.eps));
