@@ -175,9 +175,8 @@ msign_status norm_run(const NormArgs& a, const NormReach& by, double bytes, cuda
     return launch(rms_norm_loop_kernel<T, Q8>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
                   stream, a);
   const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, p.block.y)));
-  auto* k = by.shift ? (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, true>
-                        : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, true>
-                                     : rms_norm_kernel<T, 4, Q8, true>)
+  // (rows that are shifted have more than 32 pieces)
+  auto* k = by.shift ? (p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, true> : rms_norm_kernel<T, 4, Q8, true>)
                      : (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, false>
                         : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, false>
                                      : rms_norm_kernel<T, 4, Q8, false>);
@@ -231,9 +230,9 @@ constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has som
 
 template <typename T, int KIND>
 auto* norm_bwd_kernel(int vpt) {
-  return vpt == 1   ? rms_norm_bwd_kernel<T, 1, KIND>
-         : vpt == 2 ? rms_norm_bwd_kernel<T, 2, KIND>
-                    : rms_norm_bwd_kernel<T, 4, KIND>;
+  if constexpr (KIND != NORM_SHIFT)  // (rows that are shifted have more than 32 pieces)
+    if (vpt == 1) return rms_norm_bwd_kernel<T, 1, KIND>;
+  return vpt == 2 ? rms_norm_bwd_kernel<T, 2, KIND> : rms_norm_bwd_kernel<T, 4, KIND>;
 }
 
 template <typename T>

@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
   constexpr int V = Elem<T>::vec, H = V / 2;
   constexpr bool FULL = KIND == NORM_FULL, SHIFT = KIND == NORM_SHIFT;
   // The second pass unpacks z and dy again, from registers, or where a thread
-  // holds many pieces from shared memory (8192 x 8192 bf16 92 us from
-  // registers, 89 so; 4096 x 16384 107 and 103; at two pieces no difference).
+  // holds four pieces from shared memory (8192 x 8192 bf16 92 us from
+  // registers, 89 so; at two pieces no difference).
   constexpr bool kReread = VPT >= 4;
   extern __shared__ __align__(128) uint8_t ring[];  // [stages][z, dy, ds][blockDim.y][cols]
   __shared__ __align__(16) float2 red[2][16];
