@@ -960,7 +960,7 @@ __device__ __forceinline__ void store_n(T* p, const float* v) {
 }
 
 // dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
-// rows of ldp elements (a multiple of 64).  HBM-bound; both are rounded to the
+// rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
 // io type here, as the operands of the products that follow.
 //
 // 64 threads of a block take 512 columns, eight each, loaded by accesses of P

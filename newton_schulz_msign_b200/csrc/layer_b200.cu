@@ -337,11 +337,12 @@ bool map_rows(CUtensorMap* tm, const void* p, CUtensorMapDataType type, int es, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of operands that this file lays out are multiples of 128 bytes apart: a
-// box's row of 128 bytes is then one line of the L2.  At 16-byte multiples
-// int8 4096 x 4096 x 4098 takes 75 us instead of 60, 2048 x 4096 x 11016 103
-// instead of 85, the gradients of 513 x 1000 x 2730 32 instead of 30.5.
-constexpr int kPitch = 128;
+// From row to row, in elements, of an operand that this file lays out: a
+// multiple of 128 bytes, so that a box's row of 128 bytes is one line of the L2
+// (at 16-byte multiples int8 4096 x 4096 x 4098 takes 75 us instead of 60, 2048
+// x 4096 x 11016 103 instead of 85, the gradients of 513 x 1000 x 2730 32
+// instead of 30.5); of 16 bytes where that would add more than a quarter.
+int64_t pitch_of(int64_t cols, int es) { return round_up(cols, (cols * es >= 512 ? 128 : 16) / es); }
 
 // An operand's rows as a tensor map takes them: where they lie, or copied
 // into the workspace.
@@ -350,7 +351,7 @@ struct Operand {
   int64_t rows, cols, ld;
   int es;
   bool direct() const { return rows_aligned(p, ld, rows, es); }
-  int64_t padded_ld() const { return round_up(cols, kPitch / es); }
+  int64_t padded_ld() const { return pitch_of(cols, es); }
   size_t padded_bytes() const { return static_cast<size_t>(rows) * padded_ld() * es; }
 };
 
@@ -606,7 +607,7 @@ void carve_ffn(Carver& cv, const FfnShape& s, const Operand& x, const Operand& w
   carve_operand(cv, x, &c->x);
   carve_operand(cv, wg, &c->wg);
   carve_operand(cv, wu, &c->wu);
-  c->dgu = backward ? cv.take(size_t(4) * s.t * round_up(s.h, kPitch / 2)) : nullptr;
+  c->dgu = backward ? cv.take(size_t(4) * s.t * pitch_of(s.h, 2)) : nullptr;
 }
 
 // Checks that the forward and the backward call share.
@@ -623,7 +624,7 @@ msign_status ffn_check(msign_dtype dtype, int act, const FfnShape& s, int64_t x_
 template <typename T>
 msign_status dact_run(const void* dh, int64_t ldh, const void* gate, const void* up, int64_t ldp_in, void* dgu,
                       const FfnShape& s, int act, cudaStream_t stream) {
-  const int64_t ldp = round_up(s.h, kPitch / 2);
+  const int64_t ldp = pitch_of(s.h, 2);
   // whether accesses of n elements reach every row
   const auto reach = [&](int n) {
     const auto in = [&](const void* p, int64_t ld) {
@@ -929,7 +930,7 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
                      : dact_run<__half>(dh, ldh, gate, up, ldpre, c.dgu, s, act, stream);
   if (st != MSIGN_OK) return st;
   const CUtensorMapDataType type = tma_type(dt, false);
-  const int64_t hp = round_up(h, kPitch / 2);
+  const int64_t hp = pitch_of(h, 2);
   const double flops = 4.0 * tokens * d * h;
   if (dx != nullptr) {
     const double bytes = 2.0 * (2.0 * tokens * h + 2.0 * h * d + static_cast<double>(tokens) * d);
