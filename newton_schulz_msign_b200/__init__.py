@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 
 from . import _lib
@@ -507,15 +508,18 @@ def _like(t, ref, name, shape=None, dtype=None):
 def _on_stream(op):
     """Runs the operator with its ``stream`` argument (a torch stream or a raw
     handle) as the current stream, so that the outputs and the workspace that
-    it allocates belong to that stream too."""
+    it allocates belong to that stream too.  The device is that of the
+    operator's first parameter, by position or by name."""
+    first = next(iter(inspect.signature(op).parameters))
+
     @functools.wraps(op)
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return op(*args, **kwargs)
         torch = _torch()
-        t = args[0] if args else next(iter(kwargs.values()), None)
+        t = args[0] if args else kwargs.get(first)
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            return op(*args, **kwargs)  # refused there
+            raise ValueError(f"{first} must be a CUDA tensor (there is no CPU path)")
         device = t.device
         if not isinstance(stream, torch.cuda.Stream):
             # (handle 0 would make ExternalStream take a new stream)

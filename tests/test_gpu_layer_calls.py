@@ -1,0 +1,58 @@
+"""Calls of the layer operators that the documentation allows beside the plain
+ones: keywords in any order on another stream, rows off 16-byte boundaries
+called twice, values outside the finite numbers.  Bounds as in
+test_gpu_layers.py."""
+
+import pytest
+import torch
+
+import layer_oracle as L
+import newton_schulz_msign_b200 as msb
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def randn(shape, seed, dtype, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+# ---------------------------------------------------------------- streams
+
+STREAM_CALLS = {
+    "norm": lambda x, w, h, q, one, **kw: msb.rms_norm(eps=1e-5, x=x, **kw),
+    "norm, None first": lambda x, w, h, q, one, **kw: msb.rms_norm(weight=None, x=x, **kw),
+    "norm, by position": lambda x, w, h, q, one, **kw: msb.rms_norm(x, **kw),
+    "norm to int8": lambda x, w, h, q, one, **kw: msb.rms_norm_q8(scale_out=None, x=x, **kw),
+    "norm gradients": lambda x, w, h, q, one, **kw: msb.rms_norm_backward(eps=1e-5, s=x, dy=x, **kw),
+    "int8 product": lambda x, w, h, q, one, **kw: msb.i8_matmul(out_dtype=FP32, b=q, a=q, a_scale=one, b_scale=one, **kw),
+    "gated block": lambda x, w, h, q, one, **kw: msb.gated_ffn(activation="gelu", x=x, w_gate=w, w_up=w, **kw),
+    "gated gradients": lambda x, w, h, q, one, **kw: msb.gated_ffn_backward(
+        activation="gelu", dh=h, x=x, w_gate=w, w_up=w, gate=h, up=h, **kw),
+}
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", list(STREAM_CALLS))
+def test_a_call_on_a_stream_comes_after_what_that_stream_does(name, raw):
+    # the inputs are written at the end of some 20 ms of products on the side stream: a call on any other reads zeros
+    call = STREAM_CALLS[name]
+    new = [randn((64, 128), 1, BF16), randn((96, 128), 2, BF16, 0.1), randn((64, 96), 3, BF16),
+           randn((64, 128), 4, FP32, 40.0).clamp(-127, 127).to(torch.int8), randn((64,), 5, FP32).abs() + 0.1]
+    want = call(*new)
+    work = torch.ones((8192, 8192), device="cuda", dtype=BF16)
+    torch.matmul(work, work)
+    now = [torch.zeros_like(t) for t in new]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(25):
+            torch.matmul(work, work)
+        for a, b in zip(now, new):
+            a.copy_(b)
+    got = call(*now, stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+        assert a is None and b is None or torch.equal(a, b)
