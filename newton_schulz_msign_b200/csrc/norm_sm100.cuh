@@ -779,7 +779,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
         off = static_cast<uint32_t>(c0 + ph) * sizeof(T);
         bytes = static_cast<uint32_t>(c1 - c0) * sizeof(T);
       }
-      const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);  // (the elements are written, too)
+      const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
+      __syncwarp();  // the lanes' elements come before the arrive that publishes them (the sum orders no memory)
       if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
       __syncwarp();
       if (mine) bulk_load(dst + off, src, bytes, &full[st]);

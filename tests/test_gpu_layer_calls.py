@@ -56,3 +56,23 @@ def test_a_call_on_a_stream_comes_after_what_that_stream_does(name, raw):
     side.synchronize()
     for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
         assert a is None and b is None or torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- rows off 16-byte boundaries
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("cols", [257, 1001, 2046])
+@pytest.mark.parametrize("rows", [1, 2, 3])
+def test_norm_gradients_whose_row_is_its_edges(dtype, cols, rows):
+    # everything but the few elements before the first and behind the last 16-byte boundary is zero, in launches where
+    # each row is the first or the last of its matrix: what the statistic sees is stored by single lanes
+    edge = 16 // dtype.itemsize - 1
+    s, dy, w = randn((rows, cols), 10, dtype), randn((rows, cols), 11, dtype), randn((cols,), 12, dtype)
+    s[:, edge:-edge] = 0
+    dy[:, edge:-edge] = 0
+    for _ in range(20):
+        dx, dw = msb.rms_norm_backward(dy, s, w, eps=1e-5)
+        wx, ww, mx, mw = L.rms_backward(dy, s, w, None, 1e-5)
+        assert L.worst(dx, wx, wx.abs() * L.U[dtype] + mx * 200 * 2.0 ** -24 + L.TINY[dtype]) <= 1
+        assert L.worst(dw, ww, ww.abs() * L.U[dtype] + mw * 200 * 2.0 ** -24 + L.TINY[dtype]) <= 1
+    msb.sync_status()

@@ -3,11 +3,16 @@ without a GPU: streams by keyword, buffers that share memory, addresses, and
 the launch plans of the widest rows."""
 
 import contextlib
+import os
+import re
 
 import pytest
 import torch
 
 import newton_schulz_msign_b200 as msb
+
+
+CSRC = os.path.join(os.path.dirname(msb.__file__), "csrc")
 
 
 class Placed(torch.Tensor):
@@ -77,3 +82,14 @@ def test_a_stream_without_a_device_tensor_is_refused():
               lambda: msb.rms_norm(weight=None, stream=5)):
         with pytest.raises(ValueError, match="x must be a CUDA tensor"):
             f()
+
+
+def test_edge_elements_are_published_in_order():
+    # The lanes of a warp store a row's edge elements, one lane arrives on the barrier that the readers wait for: between
+    # the two every path needs a barrier of the warp that orders memory (shuffles and reductions order none).  No run
+    # shows it, since one warp's stores happen to land in order.
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "norm_sm100.cuh")).read())
+    fill = text[text.index("const auto fill = "):]
+    stores = [m.end() for m in re.finditer(r"d\[c\] = src\[c\];", fill)]
+    arrive = fill.index("mbar_arrive_expect_tx", stores[-1])
+    assert len(stores) == 2 and "__syncwarp();" in fill[stores[-1]:arrive]
