@@ -19,7 +19,7 @@ LIB_NAME = "libmsign_b200.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("msign_b200.cu", "layer_b200.cu")]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in ("gemm_sm100.cuh", "elementwise.cuh", "ptx_sm100.cuh",
-                                                   "host_sm100.cuh", "norm_sm100.cuh", "dense_sm100.cuh")] + [
+                                                   "host_sm100.cuh", "norm_plan.h", "norm_sm100.cuh", "dense_sm100.cuh")] + [
     os.path.join(ROOT, "include", "msign_b200.h")]
 
 NVCC_FLAGS = [

@@ -24,7 +24,6 @@ namespace {
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 // int8 products: |a b| <= 2^14, so K < 2^17 keeps every int32 sum exact
 constexpr int64_t kMaxI8K = (int64_t(1) << 17) - 1;
-constexpr int kPlanSms = 148;  // launch plans must not depend on the device: workspace sizes are host-only queries
 
 // Launch with the programmatic-dependent attribute (every kernel here waits
 // for its predecessor before it touches memory) and, where cluster > 0, that
@@ -86,15 +85,6 @@ bool countable(int64_t rows, int64_t cols) { return ceil_div(rows, 256) * ceil_d
 
 // ---------------------------------------------------------------- RMS norm
 
-// How the norms' kernels reach the rows: by 16 bytes; by 16 bytes about the
-// boundaries that the rows are off (NORM_SHIFT's condition: one phase, and rows
-// of at least 32 pieces: gradients of 8192 x 151 bf16 13 us either way, 301 21
-// and 19, 1002 46 and 29); by `pair` elements.
-struct NormReach {
-  bool vec, shift;
-  int pair;
-};
-
 struct NormMatrix {
   const void* p;
   int64_t stride;
@@ -127,60 +117,20 @@ NormReach norm_reach(std::initializer_list<NormMatrix> ms, const void* weight, b
   return {vec, !vec && shift, reach(2) ? 2 : 1};
 }
 
-struct NormPlan {
-  bool vec = false;
-  int vpt = 0;
-  dim3 block;
-};
-
-// Threads for rows of `pieces` 16-byte pieces: up to 128 pieces a warp takes
-// a row (no block barrier) and a block four, beyond that a block takes one.
-NormPlan norm_plan(int64_t pieces) {
-  NormPlan p;
-  if (pieces > int64_t(kNormMaxThreads) * kNormVpt) return p;
-  p.vec = true;
-  if (pieces <= 32 * kNormVpt) {
-    p.vpt = pieces <= 32 ? 1 : pieces <= 64 ? 2 : 4;
-    p.block = dim3(32, 4);
-    return p;
-  }
-  p.vpt = pieces <= 2 * kNormMaxThreads ? 2 : kNormVpt;
-  p.block = dim3(static_cast<unsigned>(round_up(ceil_div(pieces, p.vpt), 32)), 1);
-  return p;
-}
-
-// Threads of the *_elem kernels: a warp a row where that holds it, four rows a
-// block; else a block a row.
-dim3 elem_block(int64_t cols, int pair) {
-  const int x = static_cast<int>(round_up(ceil_div(cols, pair * kNormElems), 32));
-  return dim3(x, x == 32 ? 4 : 1);
-}
-
 template <typename T, bool Q8>
 msign_status norm_run(const NormArgs& a, const NormReach& by, double bytes, cudaStream_t stream) {
-  NormPlan p;
-  if (by.vec) p = norm_plan(a.cols / Elem<T>::vec);
-  if (by.shift) p = norm_plan(norm_row_bytes(a.cols, sizeof(T), true) / 16);
-  // Measured, the row in registers against the loop form, 8192 rows with a
-  // residual: two elements an access, bf16, 1002 columns 23 and 31 us, 4098 93
-  // and 109; fp32 4586 107 and 124; one element, bf16, 101 columns 6.7 and
-  // 14.1, 2001 63 and 65, 4099 135 and 116.
-  if (!p.vec && a.cols <= by.pair * kNormElems * kNormMaxThreads &&
-      (by.pair == 2 || sizeof(T) == 4 || a.cols <= 2048)) {
-    const dim3 block = elem_block(a.cols, by.pair);
-    return launch(by.pair == 2 ? rms_norm_elem_kernel<T, 2, Q8> : rms_norm_elem_kernel<T, 1, Q8>,
-                  dim3(static_cast<unsigned>(ceil_div(a.rows, block.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
+  const NormPlan p = norm_plan(a.cols, sizeof(T), by);
+  auto* k = rms_norm_loop_kernel<T, Q8>;
+  if (p.form == NormForm::kElems) {
+    k = by.pair == 2 ? rms_norm_elem_kernel<T, 2, Q8> : rms_norm_elem_kernel<T, 1, Q8>;
+  } else if (p.form == NormForm::kPieces) {
+    // (rows that are shifted have more than 32 pieces)
+    k = by.shift ? (p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, true> : rms_norm_kernel<T, 4, Q8, true>)
+                 : (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, false>
+                    : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, false>
+                                 : rms_norm_kernel<T, 4, Q8, false>);
   }
-  if (!p.vec)
-    return launch(rms_norm_loop_kernel<T, Q8>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
-                  stream, a);
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, p.block.y)));
-  // (rows that are shifted have more than 32 pieces)
-  auto* k = by.shift ? (p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, true> : rms_norm_kernel<T, 4, Q8, true>)
-                     : (p.vpt == 1   ? rms_norm_kernel<T, 1, Q8, false>
-                        : p.vpt == 2 ? rms_norm_kernel<T, 2, Q8, false>
-                                     : rms_norm_kernel<T, 4, Q8, false>);
-  return launch(k, grid, p.block, 0, 0, 3, 0.0, bytes, stream, a);
+  return launch(k, dim3(static_cast<unsigned>(ceil_div(a.rows, p.y))), dim3(p.x, p.y), 0, 0, 3, 0.0, bytes, stream, a);
 }
 
 msign_status norm_call(const void* x, const void* residual, const void* weight, void* y, void* sum_out, float* scale,
@@ -221,13 +171,6 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
   return q8 ? norm_run<float, true>(a, by, bytes, s) : norm_run<float, false>(a, by, bytes, s);
 }
 
-// Partial rows of dw that the gradients leave at most: four blocks an SM.
-constexpr int64_t kDwParts = 4 * kPlanSms;
-constexpr int64_t kDwLoopParts = 128;  // row chunks of the loop form for rows whose sums shared memory does not hold
-constexpr int64_t kLoopSums = 12000;   // columns whose sums it does (48 KB without a raised limit)
-constexpr int kSmemMax = 232448;       // shared memory of a block
-constexpr int kNormRingMax = kSmemMax - 2048;  // (the gradients' kernel has some static shared memory too)
-
 template <typename T, int KIND>
 auto* norm_bwd_kernel(int vpt) {
   if constexpr (KIND != NORM_SHIFT)  // (rows that are shifted have more than 32 pieces)
@@ -242,59 +185,31 @@ msign_status norm_bwd_run(NormBwdArgs a, void* dw, int dw_dt, const NormReach& b
   float* part = static_cast<float*>(cv.take(sizeof(float) * std::min<int64_t>(a.rows, kDwParts) * a.cols));
   float* rstd = static_cast<float*>(cv.take(sizeof(float) * a.rows));
   a.part = dw != nullptr ? part : nullptr;
-  int64_t parts;
-  msign_status st;
+  const NormBwdPlan plan = norm_bwd_plan(a.rows, a.cols, sizeof(T), by, a.ds != nullptr, dw != nullptr);
+  const NormPlan& p = plan.p;
+  const dim3 block(p.x, p.y);
+  int64_t parts = plan.parts;
   const int pair = by.pair;
-  const int row_bytes = static_cast<int>(norm_row_bytes(a.cols, sizeof(T), by.shift));
-  const int64_t pieces = row_bytes / 16;
-  const int arrays = a.ds != nullptr ? 3 : 2;
-  if ((by.vec || by.shift) && pieces <= norm_bwd_threads(kNormBwdVpt) * kNormBwdVpt) {
-    // one or two pieces a thread as far as 256 threads a row hold it, then four
-    // (up to 512 threads: 2048 x 16001 bf16 74 us, eight pieces 81; 4096 x 4700
-    // fp32 51 and 66; 8192 x 10240 bf16 129 and 123), the block filled up with
-    // rows, and the ring as deep as the SM's blocks leave room for
-    int vpt = pieces <= 32 ? 1 : 2;
-    if (pieces > vpt * norm_bwd_threads(vpt)) vpt = kNormBwdVpt;
-    const int x = static_cast<int>(round_up(ceil_div(pieces, vpt), 32));
-    const int y = std::max(1, 256 / x);
-    const bool full = by.vec && pieces == int64_t(x) * vpt && a.rows % y == 0;  // no thread is ever idle
-    // by the kernel's registers (80 a thread; with four pieces 128, fp32 with idle threads 112)
-    int per_sm = std::min(4, (vpt <= 2 ? 768 : sizeof(T) == 4 && !full ? 576 : 512) / (x * y));
-    const int slot = arrays * y * row_bytes;
-    // (an SM has 228 KB; each block 1 KB of its own and what the kernel declares)
-    const auto depth = [&] { return std::min(kNormRing, std::min(kNormRingMax, 228 * 1024 / per_sm - 1536) / slot); };
-    int stages = depth();
-    while (stages < 2) --per_sm, stages = depth();
-    parts = std::min<int64_t>({ceil_div(a.rows, y), int64_t(kPlanSms) * per_sm, kDwParts});  // what the workspace holds
-    // a thread's rows have one phase: the rows from turn to turn are a multiple of a piece's elements apart
-    const int64_t period = std::max(1, Elem<T>::vec / y);
-    if (by.shift && parts * y < a.rows) parts = parts / period * period;
-    auto* k = by.shift ? norm_bwd_kernel<T, NORM_SHIFT>(vpt)
-              : full   ? norm_bwd_kernel<T, NORM_FULL>(vpt)
-                       : norm_bwd_kernel<T, NORM_ROWS>(vpt);
-    st = launch(k, dim3(static_cast<unsigned>(parts)), dim3(x, y), static_cast<size_t>(stages) * slot, 0, 3, 0.0,
-                bytes, stream, a, stages);
+  msign_status st;
+  if (p.form == NormForm::kPieces) {
+    auto* k = by.shift    ? norm_bwd_kernel<T, NORM_SHIFT>(p.vpt)
+              : plan.full ? norm_bwd_kernel<T, NORM_FULL>(p.vpt)
+                          : norm_bwd_kernel<T, NORM_ROWS>(p.vpt);
+    st = launch(k, dim3(static_cast<unsigned>(parts)), block, static_cast<size_t>(plan.stages) * plan.slot, 0, 3, 0.0,
+                bytes, stream, a, plan.stages);
     if (st != MSIGN_OK) return st;
-  } else if (dw != nullptr && a.cols <= kLoopSums && a.rows <= 2 * kDwParts) {
-    // few rows: one launch less (777 x 1001 fp32, phases apart: 20 us a call
-    // with the host's part, 17 so; 16384 x 1001 129 us, and 93 with the sums of
-    // dw apart)
-    parts = std::min<int64_t>(a.rows, kDwParts);
-    st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(parts)), dim3(256), sizeof(float) * a.cols, 0, 3,
+  } else if (p.form == NormForm::kLoopSums) {
+    st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(parts)), block, sizeof(float) * a.cols, 0, 3,
                 0.0, bytes, stream, a, 1);
     if (st != MSIGN_OK) return st;
   } else {
     a.rstd = dw != nullptr ? rstd : nullptr;
-    // the row in registers (8192 x 1002 bf16 46 us, by the loop 76; 4098 175
-    // and 249)
-    if (a.cols <= pair * kNormElems * kNormBwdElemThreads) {
-      const dim3 block = elem_block(a.cols, pair);
+    if (p.form == NormForm::kElems)
       st = launch(pair == 2 ? rms_norm_bwd_elem_kernel<T, 2> : rms_norm_bwd_elem_kernel<T, 1>,
-                  dim3(static_cast<unsigned>(ceil_div(a.rows, block.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
-    } else {
-      st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(256), 0, 0, 3, 0.0, bytes,
-                  stream, a, 0);
-    }
+                  dim3(static_cast<unsigned>(ceil_div(a.rows, p.y))), block, 0, 0, 3, 0.0, bytes, stream, a);
+    else
+      st = launch(rms_norm_bwd_loop_kernel<T>, dim3(static_cast<unsigned>(a.rows)), block, 0, 0, 3, 0.0, bytes, stream,
+                  a, 0);
     if (st != MSIGN_OK || dw == nullptr) return st;
     const int chunk = static_cast<int>(ceil_div(a.rows, std::min<int64_t>(a.rows, kDwLoopParts)));
     parts = ceil_div(a.rows, chunk);

@@ -30,6 +30,7 @@
 #include <cstring>
 
 #include "gemm_sm100.cuh"
+#include "norm_plan.h"
 #include "ptx_sm100.cuh"
 
 namespace msb {
@@ -155,13 +156,6 @@ __device__ __forceinline__ void unpack2(const uint4& u, f32x2 (&v)[Elem<T>::vec 
 #pragma unroll
   for (int j = 0; j < Elem<T>::vec / 2; ++j) v[j] = pair2(f[2 * j], f[2 * j + 1]);
 }
-
-constexpr int kNormMaxThreads = 1024;
-// Largest block of the gradients' kernel, by the pieces of a row that a thread
-// holds.
-__host__ __device__ constexpr int norm_bwd_threads(int vpt) { return vpt <= 2 ? 256 : 512; }
-constexpr int kNormBwdVpt = 4;  // and these at most
-constexpr int kNormVpt = 4;  // 16-byte pieces of a row that one thread holds at most
 
 struct NormArgs {
   const void *x, *r, *w;  // r, w: may be null
@@ -530,8 +524,6 @@ __device__ __forceinline__ void weight_p(const void* w, int w_f32, int c, float 
 // Rows without 16-byte alignment whose phases differ or that are short, up to
 // 8 accesses a thread: like the kernel above with P elements for a piece (piece i of thread t starts at column (i
 // blockDim.x + t) P, so that a warp's accesses lie side by side).
-constexpr int kNormElems = 8;
-
 template <typename T, int P, bool Q8>
 __global__ void __launch_bounds__(kNormMaxThreads) rms_norm_elem_kernel(const NormArgs a) {
   constexpr int E = kNormElems;
@@ -719,13 +711,7 @@ __device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w,
 // the barrier and spilled.  A running pointer to dz's row costs registers
 // (53), four blocks an SM spill (59), a warp a row leaves the instruction
 // caches (68).
-constexpr int kNormRing = 8;
 enum { NORM_ROWS, NORM_FULL, NORM_SHIFT };
-
-// A row in shared memory: with SHIFT as it lies about its 16-byte boundaries.
-__host__ __device__ inline uint32_t norm_row_bytes(int cols, int es, bool shift) {
-  return shift ? (static_cast<uint32_t>(cols) * es + 31u - es) / 16u * 16u : static_cast<uint32_t>(cols) * es;
-}
 
 template <typename T, int VPT, int KIND>
 __global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
@@ -743,7 +729,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
   const int ny = blockDim.y, nwarp = blockDim.x >> 5;       // rows of a group, warps of a row
   const int warp = threadIdx.y * nwarp + (threadIdx.x >> 5);
   const int red0 = threadIdx.y * ((nwarp + 1) & ~1);        // where this row's warps leave their sums, in pairs
-  const uint32_t row_bytes = norm_row_bytes(a.cols, sizeof(T), SHIFT);
+  const uint32_t row_bytes = norm_row_bytes<uint32_t>(a.cols, sizeof(T), SHIFT);
   const int arrays = a.ds != nullptr ? 3 : 2;
   const uint32_t slot = static_cast<uint32_t>(arrays * ny) * row_bytes;
   const long long step = static_cast<long long>(gridDim.x) * ny;
@@ -987,8 +973,6 @@ __global__ void __launch_bounds__(norm_bwd_threads(VPT), VPT <= 2 ? 3 : 1)
 // Rows without 16-byte alignment whose phases differ or that are short, P
 // elements an access, up to 8 a thread: dz
 // and the row statistic in one pass, a row a block (or a warp a row).
-constexpr int kNormBwdElemThreads = 512;
-
 template <typename T, int P>
 __global__ void __launch_bounds__(kNormBwdElemThreads) rms_norm_bwd_elem_kernel(const NormBwdArgs a) {
   constexpr int E = kNormElems;

@@ -5,6 +5,8 @@ the launch plans of the widest rows."""
 import contextlib
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -93,3 +95,75 @@ def test_edge_elements_are_published_in_order():
     stores = [m.end() for m in re.finditer(r"d\[c\] = src\[c\];", fill)]
     arrive = fill.index("mbar_arrive_expect_tx", stores[-1])
     assert len(stores) == 2 and "__syncwarp();" in fill[stores[-1]:arrive]
+
+
+# ---------------------------------------------------------------- launch plans
+
+PIECES, ELEMS, LOOP, LOOP_SUMS = range(4)
+RING_BYTES, DW_PARTS = 232448 - 2048, 592
+
+
+@pytest.fixture(scope="module")
+def norm_plans(tmp_path_factory):
+    """The plans of a list of (rows, cols, bytes of an element, whole pieces, shifted pieces, elements an access)."""
+    compiler = shutil.which("g++") or shutil.which("c++")
+    if compiler is None:
+        pytest.skip("no C++ compiler")
+    exe = str(tmp_path_factory.mktemp("plan") / "norm_plan")
+    src = os.path.join(os.path.dirname(os.path.abspath(__file__)), "c", "norm_plan.cpp")
+    subprocess.run([compiler, "-std=c++17", "-Wall", "-Wextra", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover",
+                    "-static-libubsan", "-I", CSRC, src, "-o", exe], check=True)
+
+    def plans(cases):
+        run = subprocess.run([exe], input="\n".join(" ".join(str(int(v)) for v in c) for c in cases), capture_output=True,
+                             text=True, timeout=60)
+        assert run.returncode == 0, run.stderr
+        return [tuple(int(v) for v in line.split()) for line in run.stdout.splitlines()]
+
+    return plans
+
+
+def reaches(cols, es):
+    """How rows of this width may be reached: whole pieces, shifted pieces, elements by two and one."""
+    if cols % (16 // es) == 0:
+        yield 1, 0, 2
+    if cols >= 32 * (16 // es):
+        yield 0, 1, 1 + (cols % 2 == 0)
+    yield 0, 0, 1 + (cols % 2 == 0)
+
+
+@pytest.mark.parametrize("es", [2, 4])
+def test_the_widest_rows_take_the_loop(norm_plans, es):
+    # rows of 2^31 and 2^32 bytes: their size does not fit 32 bits
+    cases = [(rows, cols, es) + by for cols in (2 ** 28, 2 ** 29 - 8, 2 ** 29, 2 ** 29 + 1, 2 ** 30 - 8, 2 ** 30 - 6, 2 ** 30 - 1, 2 ** 30)
+             for rows in (1, 3) for by in reaches(cols, es)]
+    for c, p in zip(cases, norm_plans(cases)):
+        assert p[0] == LOOP and p[4] == LOOP and p[2:4] == p[6:8] == (256, 1), (c, p)
+
+
+@pytest.mark.parametrize("es", [2, 4])
+def test_every_plan_holds_its_rows(norm_plans, es):
+    widths = sorted({w for n in (1, 8, 32, 64, 101, 128, 256, 257, 500, 1000, 1024, 2048, 2730, 3000, 4096, 6144, 8192, 10240, 12000,
+                                 16384, 20000, 32768, 40000, 10 ** 6) for w in (n - 1, n, n + 1, n + 8) if w > 0})
+    cases = [(rows, cols, es) + by for cols in widths for rows in (1, 2, 7, 64, 777, 1184, 1185, 8192, 10 ** 6) for by in reaches(cols, es)]
+    plans = norm_plans(cases)
+    assert len(plans) == len(cases)
+    for c, p in zip(cases, plans):
+        rows, cols, _, vec, shift, pair = c
+        # the 16-byte units that a row can touch, in bytes
+        row = (cols * es + 31 - es) // 16 * 16 if shift else cols * es
+        form, vpt, x, y = p[:4]
+        assert x % 32 == 0 and x * y <= 1024 and (y == 1 or x == 32), (c, p)
+        assert {PIECES: x * vpt * 16 >= row, ELEMS: x * 8 * pair >= cols, LOOP: (x, y) == (256, 1)}[form], (c, p)
+        form, vpt, x, y, full, slot, stages, parts = p[4:]
+        if form == PIECES:
+            assert x * vpt * 16 >= row and x * y <= (256 if vpt <= 2 else 512) and x % 32 == 0, (c, p)
+            assert slot == 3 * y * row and 2 <= stages <= 8 and stages * slot <= RING_BYTES, (c, p)
+            assert 1 <= parts <= min(rows, DW_PARTS) and y * cols * 4 <= stages * slot, (c, p)
+            # whole blocks where the plan says so, and one phase a thread where rows are shifted
+            assert not full or (rows % y == 0 and x * vpt * 16 == row)
+            assert not shift or parts * y >= rows or parts * y % (16 // es) == 0, (c, p)
+        elif form == ELEMS:
+            assert x * 8 * pair >= cols and x * y <= 512, (c, p)
+        elif form == LOOP_SUMS:
+            assert cols <= 12000 and 1 <= parts <= min(rows, DW_PARTS), (c, p)
