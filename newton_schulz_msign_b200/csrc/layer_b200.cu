@@ -665,6 +665,7 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
   if (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr) return MSIGN_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, i8_matmul_workspace_size(m, n, k, a, a_stride, b, b_stride)))
     return MSIGN_ERR_WORKSPACE;
+  if (is_one_of(out, {a, b, a_scale, b_scale})) return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   msign_status st = layer_state(&dev);
   if (st != MSIGN_OK) return st;

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import newton_schulz_msign_b200 as msb
+from newton_schulz_msign_b200 import _lib, build
 
 
 CSRC = os.path.join(os.path.dirname(msb.__file__), "csrc")
@@ -167,3 +168,26 @@ def test_every_plan_holds_its_rows(norm_plans, es):
             assert x * 8 * pair >= cols and x * y <= 512, (c, p)
         elif form == LOOP_SUMS:
             assert cols <= 12000 and 1 <= parts <= min(rows, DW_PARTS), (c, p)
+
+
+# ---------------------------------------------------------------- buffers that share memory
+
+B, H, F = _lib.BF16, _lib.FP16, _lib.FP32
+BAD, OK = _lib.ERR_INVALID_ARG, _lib.OK
+
+
+def at(i):
+    """An address that no refused call touches."""
+    return (1 << 20) + (i << 16)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.lib()
+
+
+@pytest.mark.parametrize("out", [0, 1, 2, 3])
+def test_i8_matmul_refuses_an_input_as_its_output(lib, out):
+    # (fp32 out of the operands' size in bytes fits either of them)
+    assert lib.i8_matmul(at(0), at(1), at(2), at(3), at(out), F, 4, 64, 256, 0, 0, 0, None, 0, None) == BAD
