@@ -144,7 +144,8 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
     return MSIGN_ERR_INVALID_ARG;
   if (residual == nullptr && sum_out != nullptr) return MSIGN_ERR_INVALID_ARG;
   if (rows > 0 && cols > 0 &&
-      (is_one_of(y, {sum_out, weight}) || is_one_of(sum_out, {weight}) || (q8 && is_one_of(y, {x, residual}))))
+      (is_one_of(y, {sum_out, weight}) || is_one_of(sum_out, {weight}) || (q8 && is_one_of(y, {x, residual})) ||
+       is_one_of(scale, {x, residual, weight, y, sum_out})))
     return MSIGN_ERR_INVALID_ARG;
   if (weight != nullptr && w_dtype != io_dtype && w_dtype != MSIGN_FP32) return MSIGN_ERR_UNSUPPORTED;
   if (rows == 0 || cols == 0) return MSIGN_OK;

@@ -191,3 +191,8 @@ def lib():
 def test_i8_matmul_refuses_an_input_as_its_output(lib, out):
     # (fp32 out of the operands' size in bytes fits either of them)
     assert lib.i8_matmul(at(0), at(1), at(2), at(3), at(out), F, 4, 64, 256, 0, 0, 0, None, 0, None) == BAD
+
+
+@pytest.mark.parametrize("scale", [0, 1, 2, 3, 4])
+def test_rms_norm_q8_refuses_another_buffer_as_its_scales(lib, scale):
+    assert lib.rms_norm_q8(at(0), at(1), at(2), at(3), at(scale), at(4), F, F, 4, 64, 0, 0, 0, 0, 1e-6, None) == BAD
