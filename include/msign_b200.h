@@ -465,11 +465,12 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
  * of the rounded sum, which is what rms_norm_backward is given.  Squares are
  * summed and y is formed in fp32.
  *   residual, sum_out  may be NULL; sum_out needs a residual, and may be x
- *                      or residual itself (same address and stride)
+ *                      or residual itself (same address and, for more than
+ *                      one row, same stride: MSIGN_ERR_INVALID_ARG else)
  *   weight             cols elements of w_dtype (io_dtype or MSIGN_FP32), or
  *                      NULL for ones
- *   y                  may be x or residual itself, where that is not
- *                      sum_out; no other overlap is allowed
+ *   y                  may be x or residual itself on the same terms, where
+ *                      that is not sum_out; no other overlap is allowed
  *   eps                >= 0 and finite (a row of zeros with eps 0 gives NaN) */
 msign_status rms_norm(const void *x, const void *residual, const void *weight, void *y, void *sum_out,
                       msign_dtype io_dtype, msign_dtype w_dtype, int64_t rows, int64_t cols, int64_t x_stride,

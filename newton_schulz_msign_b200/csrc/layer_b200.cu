@@ -151,6 +151,13 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
   if (rows == 0 || cols == 0) return MSIGN_OK;
   if (x == nullptr || y == nullptr) return MSIGN_ERR_INVALID_ARG;
   if (rows > kMaxDim || cols > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  // an output over an input: row over row, or one row's block would write what another still reads
+  const auto apart = [&](const void* o, int64_t o_stride, const void* in, int64_t in_stride) {
+    return rows > 1 && o == in && o != nullptr && stride_of(o_stride, cols) != stride_of(in_stride, cols);
+  };
+  if (apart(y, y_stride, x, x_stride) || apart(y, y_stride, residual, r_stride) ||
+      apart(sum_out, s_stride, x, x_stride) || apart(sum_out, s_stride, residual, r_stride))
+    return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   msign_status st = device_state(&dev);
   if (st != MSIGN_OK) return st;

@@ -196,3 +196,22 @@ def test_i8_matmul_refuses_an_input_as_its_output(lib, out):
 @pytest.mark.parametrize("scale", [0, 1, 2, 3, 4])
 def test_rms_norm_q8_refuses_another_buffer_as_its_scales(lib, scale):
     assert lib.rms_norm_q8(at(0), at(1), at(2), at(3), at(scale), at(4), F, F, 4, 64, 0, 0, 0, 0, 1e-6, None) == BAD
+
+
+IN_PLACE = [  # over which input, with which strides (x, residual, y, sum)
+    (dict(y=0), (0, 0, 72, 0)), (dict(y=0), (72, 0, 0, 0)), (dict(y=1), (0, 80, 72, 0)), (dict(y=1), (72, 0, 72, 0)),
+    (dict(s=0), (0, 0, 0, 72)), (dict(s=0), (80, 0, 0, 72)), (dict(s=1), (0, 72, 0, 0)), (dict(s=1), (72, 0, 0, 72))]
+
+
+def in_place_status(lib, outs, strides, rows, q8=False):
+    y, s = at(outs.get("y", 3)), at(outs.get("s", 4))
+    if q8:
+        return lib.rms_norm_q8(at(0), at(1), at(2), y, at(5), s, B, B, rows, 64, *strides, 1e-6, None)
+    return lib.rms_norm(at(0), at(1), at(2), y, s, B, B, rows, 64, *strides, 1e-6, None)
+
+
+@pytest.mark.parametrize("outs,strides", IN_PLACE)
+def test_rms_norm_in_place_needs_the_inputs_row_stride(lib, outs, strides):
+    assert in_place_status(lib, outs, strides, 4) == BAD
+    if "s" in outs:
+        assert in_place_status(lib, outs, strides, 4, q8=True) == BAD
