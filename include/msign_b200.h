@@ -446,7 +446,8 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
  * A matrix argument of these entry points is `rows` rows of dense elements,
  * a row stride (in elements) apart: 0 means back to back, otherwise at least
  * the row's length (MSIGN_ERR_INVALID_ARG else).  Rows behind the last one
- * and elements between rows are neither read nor written.  Any alignment and
+ * and elements between rows are neither read nor written.  Any address
+ * that is a multiple of an element's size (MSIGN_ERR_INVALID_ARG else) and
  * any size is taken; bases on 16-byte boundaries and strides of whole 16-byte
  * pieces run fastest (a product whose operands lack that first copies them
  * into the workspace, which is what its *_workspace_size query counts).

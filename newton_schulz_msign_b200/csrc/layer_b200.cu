@@ -79,6 +79,14 @@ bool is_one_of(const void* p, std::initializer_list<const void*> others) {
   return false;
 }
 
+// Whether every address is a multiple of its element's size, which each access
+// needs (es bytes; nullptr is).
+bool on_elements(std::initializer_list<const void*> ps, int es) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % es != 0) return false;
+  return true;
+}
+
 // Whether a product's 256 x 128 tiles can be counted in an int (the kernels'
 // tile numbers): looked at before anything is enqueued.
 bool countable(int64_t rows, int64_t cols) { return ceil_div(rows, 256) * ceil_div(cols, 128) <= INT32_MAX / 4; }
@@ -151,6 +159,10 @@ msign_status norm_call(const void* x, const void* residual, const void* weight, 
   if (rows == 0 || cols == 0) return MSIGN_OK;
   if (x == nullptr || y == nullptr) return MSIGN_ERR_INVALID_ARG;
   if (rows > kMaxDim || cols > kMaxDim) return MSIGN_ERR_UNSUPPORTED;
+  if (!on_elements({x, residual, sum_out}, dtype_size(to_dt(io_dtype))) ||
+      !on_elements({y}, q8 ? 1 : dtype_size(to_dt(io_dtype))) || !on_elements({weight}, dtype_size(to_dt(w_dtype))) ||
+      !on_elements({scale}, 4))
+    return MSIGN_ERR_INVALID_ARG;
   // an output over an input: row over row, or one row's block would write what another still reads
   const auto apart = [&](const void* o, int64_t o_stride, const void* in, int64_t in_stride) {
     return rows > 1 && o == in && o != nullptr && stride_of(o_stride, cols) != stride_of(in_stride, cols);
@@ -624,6 +636,7 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   const int wdt = to_dt(w_dtype);
   if (rows == 0) return zero_rows(dw, cols, 1, cols, dtype_size(wdt), s);  // a sum over no rows
   if (dy == nullptr || sum == nullptr || dx == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (!on_elements({dy, sum, dsum, dx}, es) || !on_elements({weight, dw}, dtype_size(wdt))) return MSIGN_ERR_INVALID_ARG;
   if (is_one_of(dx, {dy, sum, weight, dsum, dw}) || is_one_of(dw, {dy, sum, weight, dsum})) return MSIGN_ERR_INVALID_ARG;
   if (dw != nullptr && !workspace_ok(workspace, workspace_bytes, rms_norm_backward_workspace_size(rows, cols)))
     return MSIGN_ERR_WORKSPACE;
@@ -671,6 +684,7 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
   const int64_t ldo = stride_of(out_stride, n);
   if (k == 0) return zero_rows(out, ldo, m, n, oes, stream);
   if (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (!on_elements({a_scale, b_scale}, 4) || !on_elements({out}, oes)) return MSIGN_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes, i8_matmul_workspace_size(m, n, k, a, a_stride, b, b_stride)))
     return MSIGN_ERR_WORKSPACE;
   if (is_one_of(out, {a, b, a_scale, b_scale})) return MSIGN_ERR_INVALID_ARG;
@@ -750,6 +764,7 @@ msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void
     return MSIGN_OK;
   }
   if (x == nullptr || w_gate == nullptr || w_up == nullptr) return MSIGN_ERR_INVALID_ARG;
+  if (!on_elements({x, w_gate, w_up, out, gate_out, up_out}, 2)) return MSIGN_ERR_INVALID_ARG;
   if (is_one_of(out, {x, w_gate, w_up, gate_out, up_out}) || is_one_of(gate_out, {x, w_gate, w_up, up_out}) ||
       is_one_of(up_out, {x, w_gate, w_up}))
     return MSIGN_ERR_INVALID_ARG;
@@ -833,6 +848,8 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
     return zero_rows(dw_up, lddw, h, d, dtype_size(gdt), stream);
   }
   if (dh == nullptr || x == nullptr || w_gate == nullptr || w_up == nullptr || gate == nullptr || up == nullptr)
+    return MSIGN_ERR_INVALID_ARG;
+  if (!on_elements({dh, x, w_gate, w_up, gate, up, dx}, 2) || !on_elements({dw_gate, dw_up}, dtype_size(gdt)))
     return MSIGN_ERR_INVALID_ARG;
   if (is_one_of(dx, {dh, x, w_gate, w_up, gate, up, dw_gate, dw_up}) ||
       is_one_of(dw_gate, {dh, x, w_gate, w_up, gate, up, dw_up}) || is_one_of(dw_up, {dh, x, w_gate, w_up, gate, up}))

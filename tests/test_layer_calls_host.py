@@ -215,3 +215,46 @@ def test_rms_norm_in_place_needs_the_inputs_row_stride(lib, outs, strides):
     assert in_place_status(lib, outs, strides, 4) == BAD
     if "s" in outs:
         assert in_place_status(lib, outs, strides, 4, q8=True) == BAD
+
+
+# ---------------------------------------------------------------- addresses between elements
+
+def norm_at(lib, i, off, io=B, wd=F, q8=False):
+    """The norm with its i-th buffer (x, residual, weight, y, sum, scales) `off` bytes further on."""
+    p = [at(j) + (off if j == i else 0) for j in range(6)]
+    if q8:
+        return lib.rms_norm_q8(p[0], p[1], p[2], p[3], p[5], p[4], io, wd, 4, 64, 0, 0, 0, 0, 1e-6, None)
+    return lib.rms_norm(*p[:5], io, wd, 4, 64, 0, 0, 0, 0, 1e-6, None)
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_rms_norm_refuses_addresses_between_elements(lib, i):
+    assert norm_at(lib, i, 1) == BAD and norm_at(lib, i, 2, io=F) == BAD
+    if i != 3:
+        assert norm_at(lib, i, 1, q8=True) == BAD
+    if i == 2:  # the weight's own type counts
+        assert norm_at(lib, i, 2) == BAD
+    assert norm_at(lib, 5, 2, q8=True) == BAD
+
+
+@pytest.mark.parametrize("i", range(6))
+def test_rms_norm_backward_refuses_addresses_between_elements(lib, i):
+    p = [at(j) + (1 if j == i else 0) for j in range(6)]  # dy, s, w, dsum, dx, dw
+    size = lib.rms_norm_backward_workspace_size(4, 64)
+    assert lib.rms_norm_backward(*p, B, B, 4, 64, 0, 0, 0, 0, 1e-6, at(6), size, None) == BAD
+
+
+@pytest.mark.parametrize("i,off", [(1, 2), (3, 2), (4, 1)])
+def test_i8_matmul_refuses_addresses_between_elements(lib, i, off):
+    p = [at(j) + (off if j == i else 0) for j in range(5)]
+    assert lib.i8_matmul(*p, B, 4, 64, 256, 0, 0, 0, None, 0, None) == BAD
+
+
+@pytest.mark.parametrize("i", range(9))
+def test_gated_ffn_refuses_addresses_between_elements(lib, i):
+    p = [at(j) + (1 if j == i else 0) for j in range(9)]
+    big = 1 << 20
+    if i < 6:  # x, the weights, out, gate, up
+        assert lib.gated_ffn(*p[:6], B, 0, 4, 64, 64, 0, 0, 0, 0, at(9), big, None) == BAD
+    # dh, x, the weights, gate, up, dx, the weights' gradients
+    assert lib.gated_ffn_backward(*p, B, B, 0, 4, 64, 64, 0, 0, 0, 0, 0, 0, at(9), big, None) == BAD
