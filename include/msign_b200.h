@@ -446,11 +446,15 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
  * A matrix argument of these entry points is `rows` rows of dense elements,
  * a row stride (in elements) apart: 0 means back to back, otherwise at least
  * the row's length (MSIGN_ERR_INVALID_ARG else).  Rows behind the last one
- * and elements between rows are neither read nor written.  Any address
- * that is a multiple of an element's size (MSIGN_ERR_INVALID_ARG else) and
- * any size is taken; bases on 16-byte boundaries and strides of whole 16-byte
- * pieces run fastest (a product whose operands lack that first copies them
- * into the workspace, which is what its *_workspace_size query counts).
+ * are neither read nor written.  Elements between rows are never written and
+ * no result depends on them; where a row is off 16-byte boundaries, up to 15
+ * bytes of them on either side are read with the row and discarded (a caller
+ * that writes them at the same time races with that read).
+ * Any address that is a multiple of an element's size (MSIGN_ERR_INVALID_ARG
+ * else) and any size is taken; bases on 16-byte boundaries and strides of
+ * whole 16-byte pieces run fastest (a product whose operands lack that first
+ * copies them into the workspace, which is what its *_workspace_size query
+ * counts).
  * Row counts and widths are at most 2^30, and a product has at most 2^29
  * tiles of 256 x 128 outputs (MSIGN_ERR_UNSUPPORTED beyond).
  * An output at the address of another buffer of its call is refused

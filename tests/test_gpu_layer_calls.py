@@ -76,3 +76,29 @@ def test_norm_gradients_whose_row_is_its_edges(dtype, cols, rows):
         assert L.worst(dx, wx, wx.abs() * L.U[dtype] + mx * 200 * 2.0 ** -24 + L.TINY[dtype]) <= 1
         assert L.worst(dw, ww, ww.abs() * L.U[dtype] + mw * 200 * 2.0 ** -24 + L.TINY[dtype]) <= 1
     msb.sync_status()
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 3.0])
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_no_result_depends_on_what_lies_between_rows(fill, pad):
+    # rows whose neighbours' bytes are read with them, in every operator that does so
+    def apart(t, value):
+        big = torch.full((t.shape[0], t.shape[1] + pad), value, device="cuda").to(t.dtype)
+        big[:, :t.shape[1]] = t
+        return big[:, :t.shape[1]]
+
+    x, dy, ds = (randn((37, 1001), s, BF16) for s in (20, 21, 22))
+    w, wg, wu = randn((1001,), 23, BF16), randn((50, 1001), 24, BF16, 0.03), randn((50, 1001), 25, BF16, 0.03)
+    q, b = (randn((n, 1001), 26 + n, FP32, 40.0).clamp(-127, 127).to(torch.int8) for n in (37, 50))
+    one = torch.ones(50, device="cuda")
+
+    def run(value):
+        lay = lambda t: apart(t, value if t.is_floating_point() else 77)  # noqa: E731
+        z = lay(torch.zeros_like(x))
+        out = [*msb.rms_norm(lay(x), w, lay(ds)), *msb.rms_norm_q8(lay(x), w, lay(ds))]
+        out += msb.rms_norm_backward(lay(dy), lay(x), w, dsum=lay(ds), dx_out=z)
+        out += [*msb.gated_ffn(lay(x), lay(wg), lay(wu), save=True), msb.i8_matmul(lay(q), one[:37], lay(b), one)]
+        return [t.clone() for t in out]
+
+    for a, c in zip(run(0.0), run(fill)):
+        assert torch.equal(a, c)
