@@ -128,8 +128,8 @@ __device__ __forceinline__ float2 act_grad(float g) {
     const float c = 0.5f * erfcf(-0.70710678118654752f * g);
     return make_float2(g * c, fmaf(g * 0.3989422804014327f, __expf(-0.5f * g * g), c));
   }
-  // past |g| = 30 p is 0 or 1 to the last bit: the clamp only keeps the cube finite
-  const float c = fminf(fmaxf(g, -30.0f), 30.0f);
+  // past |g| = 30 p is 0 or 1 to the last bit: the clamp only keeps the cube finite (and keeps a NaN)
+  const float c = fabsf(g) > 30.0f ? copysignf(30.0f, g) : g;
   const float p = __fdividef(1.0f, 1.0f + __expf(-2.0f * kGeluC * fmaf(kGeluA * c * c, c, c)));
   return make_float2(g * p, fmaf(2.0f * p * (1.0f - p), kGeluC * fmaf(3.0f * kGeluA * c * c, c, c), p));
 }

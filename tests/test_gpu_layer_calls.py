@@ -102,3 +102,20 @@ def test_no_result_depends_on_what_lies_between_rows(fill, pad):
 
     for a, c in zip(run(0.0), run(fill)):
         assert torch.equal(a, c)
+
+
+# ---------------------------------------------------------------- values outside the finite numbers
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("h", [64, 101])
+def test_a_nan_gate_reaches_its_gradients(dtype, act, h):
+    # a NaN gate makes dg NaN whatever the activation: dx of its token and dWg of its unit, and nothing else of them
+    t, d = 40, 64
+    x, wg, wu = randn((t, d), 30, dtype), randn((h, d), 31, dtype, 0.1), randn((h, d), 32, dtype, 0.1)
+    gate, up, dh = randn((t, h), 33, dtype), randn((t, h), 34, dtype), randn((t, h), 35, dtype)
+    gate[3, 7] = float("nan")
+    dx, dwg, dwu = msb.gated_ffn_backward(dh, x, wg, wu, gate, up, activation=act)
+    for g, i in ((dx, 3), (dwg, 7), (dwu, 7)):
+        keep = [j for j in range(g.shape[0]) if j != i]
+        assert bool(torch.isnan(g[i]).all()) and bool(torch.isfinite(g[keep]).all())
