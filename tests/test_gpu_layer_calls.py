@@ -119,3 +119,31 @@ def test_a_nan_gate_reaches_its_gradients(dtype, act, h):
     for g, i in ((dx, 3), (dwg, 7), (dwu, 7)):
         keep = [j for j in range(g.shape[0]) if j != i]
         assert bool(torch.isnan(g[i]).all()) and bool(torch.isfinite(g[keep]).all())
+
+
+# ---------------------------------------------------------------- the longest rows
+
+@pytest.mark.parametrize("cols,lead", [(2 ** 28, 0), (2 ** 28 - 3, 1)])
+def test_sums_of_very_long_rows(cols, lead):
+    # 2^20 terms a thread, added in runs: 1024 terms, 1024 runs and 13 joins of halved weight (the root), and five more
+    # operations.  (One sum all along is off by several times this bound.)
+    rel = ((1024 + 1024 + 13) / 2 + 5) * 2.0 ** -24
+    x = randn((cols + lead,), 40, BF16)[lead:]
+    dy = randn((cols + lead,), 41, BF16)[lead:]
+    y, scale = msb.rms_norm(x), msb.rms_norm_q8(x)[1]
+    dx = msb.rms_norm_backward(dy, x)[0]
+    part = 2 ** 26
+    ss = sum(float((x[i:i + part].double() ** 2).sum()) for i in range(0, cols, part))
+    dot = sum(float((x[i:i + part].double() * dy[i:i + part].double()).sum()) for i in range(0, cols, part))
+    mag = sum(float((x[i:i + part].double() * dy[i:i + part].double()).abs().sum()) for i in range(0, cols, part))
+    rstd = (ss / cols + 1e-6) ** -0.5
+    amax = float(x.abs().max()) * rstd
+    assert abs(float(scale) - amax / 127) <= amax / 127 * rel
+    for i in range(0, cols, part):
+        z, g = x[i:i + part].double(), dy[i:i + part].double()
+        want = z * rstd
+        assert L.worst(y[i:i + part], want, want.abs() * (L.U[BF16] + rel) + L.TINY[BF16]) <= 1
+        m = rstd / cols
+        want = rstd * (g - z * rstd * (dot * m))
+        bound = rstd * (g.abs() + z.abs() * rstd * mag * m) * 2 * rel
+        assert L.worst(dx[i:i + part], want, want.abs() * L.U[BF16] + bound + L.TINY[BF16]) <= 1
