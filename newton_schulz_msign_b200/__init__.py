@@ -528,7 +528,9 @@ def _on_stream(op):
             raise ValueError(f"the stream is on {stream.device}, the call runs on {device}")
         with torch.cuda.stream(stream):
             return op(*args, **kwargs)
-    call.__doc__ += "\n\n    ``stream``: the stream to run on, for the outputs too (default: the current one)."
+    # (python -OO leaves no docstring to add to)
+    if op.__doc__:
+        call.__doc__ = op.__doc__ + "\n\n    ``stream``: the stream to run on, for the outputs too (default: the current one)."
     return call
 
 

@@ -7,6 +7,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -258,3 +259,13 @@ def test_gated_ffn_refuses_addresses_between_elements(lib, i):
         assert lib.gated_ffn(*p[:6], B, 0, 4, 64, 64, 0, 0, 0, 0, at(9), big, None) == BAD
     # dh, x, the weights, gate, up, dx, the weights' gradients
     assert lib.gated_ffn_backward(*p, B, B, 0, 4, 64, 64, 0, 0, 0, 0, 0, 0, at(9), big, None) == BAD
+
+
+# ---------------------------------------------------------------- the package
+
+@pytest.mark.parametrize("flags", [[], ["-O"], ["-OO"]])
+def test_the_package_imports_without_docstrings(flags):
+    root = os.path.dirname(os.path.dirname(msb.__file__))
+    run = subprocess.run([sys.executable, *flags, "-c", "import newton_schulz_msign_b200 as m; m.rms_norm, m.gated_ffn"],
+                         cwd=root, capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stderr
