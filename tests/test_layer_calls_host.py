@@ -269,3 +269,20 @@ def test_the_package_imports_without_docstrings(flags):
     run = subprocess.run([sys.executable, *flags, "-c", "import newton_schulz_msign_b200 as m; m.rms_norm, m.gated_ffn"],
                          cwd=root, capture_output=True, text=True, timeout=120)
     assert run.returncode == 0, run.stderr
+
+
+def test_the_current_stream_without_torchs_own_lookup(monkeypatch):
+    class Current:
+        cuda_stream = 1234
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: Current())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(msb, "_torch_module", None)
+    monkeypatch.setattr(msb, "_raw_stream", None, raising=False)
+
+    class On:
+        def get_device(self):
+            return 0
+
+    assert msb._call(lambda *a: a, On(), "x") == ("x", 1234)
