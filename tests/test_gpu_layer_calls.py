@@ -147,3 +147,46 @@ def test_sums_of_very_long_rows(cols, lead):
         want = rstd * (g - z * rstd * (dot * m))
         bound = rstd * (g.abs() + z.abs() * rstd * mag * m) * 2 * rel
         assert L.worst(dx[i:i + part], want, want.abs() * L.U[BF16] + bound + L.TINY[BF16]) <= 1
+
+
+# ---------------------------------------------------------------- the same call twice
+
+# (lead, pad, apart) as in test_gpu_layers.py
+OFF = [(0, 0, 0), (1, 0, 1), (3, 0, 0), (5, 1, 0), (7, 2, 3), (2, 5, 0)]
+
+
+def inside(shape, dtype, lead, pad, seed=None):
+    """Rows ``pad`` elements apart, ``lead`` elements into a larger buffer."""
+    rows, cols = shape
+    big = torch.zeros(lead + rows * (cols + pad), device="cuda", dtype=dtype)
+    v = big.as_strided(shape, (cols + pad, 1), lead)
+    if seed is not None:
+        v.copy_(randn(shape, seed, dtype))
+    return v
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("rows,cols", [(41, 257), (600, 1003), (2500, 1003), (5, 2046), (700, 4607), (3, 16381), (300, 20001)])
+@pytest.mark.parametrize("lead,pad,apart", OFF)
+def test_norm_gradients_off_boundaries_repeat_their_bits(dtype, rows, cols, lead, pad, apart):
+    # every layout, with outputs of the inputs' layout, so that both calls take the same kernel and the same blocks
+    s, ds = inside((rows, cols), dtype, lead, pad, 50), inside((rows, cols), dtype, lead, pad, 51) if rows % 2 else None
+    dy, w = inside((rows, cols), dtype, lead + apart, pad, 52), randn((cols,), 53, dtype)
+    busy = torch.ones((2048, 2048), device="cuda", dtype=BF16)
+    side = torch.cuda.Stream()
+    first = None
+    for i in range(4):
+        if i % 2:  # beside other work, which changes the order in which blocks run
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.matmul(busy, busy)
+        dx = inside((rows, cols), dtype, lead, pad)
+        _, dw = msb.rms_norm_backward(dy, s, w, dsum=ds, dx_out=dx)
+        if first is None:
+            first = (dx, dw)
+        assert torch.equal(dx, first[0]) and torch.equal(dw, first[1])
+    torch.cuda.synchronize()
+    wx, ww, mx, mw = L.rms_backward(dy, s, w, ds, 1e-6)
+    serial = 200 + (rows + 99) // 100
+    assert L.worst(first[0], wx, wx.abs() * L.U[dtype] + mx * serial * 2.0 ** -24 + L.TINY[dtype]) <= 1
+    assert L.worst(first[1], ww, ww.abs() * L.U[dtype] + mw * serial * 2.0 ** -24 + L.TINY[dtype]) <= 1
