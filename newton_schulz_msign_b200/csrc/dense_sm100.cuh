@@ -105,9 +105,27 @@ enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// g sigmoid(v).  exp(-v) overflows to infinity for very negative v, and the
-// quotient is 0 there, as it should be.
-__device__ __forceinline__ float g_sigmoid(float g, float v) { return __fdividef(g, 1.0f + __expf(-v)); }
+// 2^x and 1 / x to a few steps of fp32, subnormal results flushed to 0.
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// g sigmoid(v) = (g / 4) / (1/4 + 2^(-v log2 e - 2)).  The quarters keep the
+// divisor's reciprocal a normal number for as long as exp(-v) is finite (1 +
+// exp(-v) reaches 2^128, and the reciprocal of anything past 2^126 flushes:
+// silu from -87.3 to -88.7 is still 1e-36); past that the product is 0, as it
+// should be.  A power of two that flushes is nothing beside the 1/4.
+__device__ __forceinline__ float g_sigmoid(float g, float v) {
+  return 0.25f * g * rcp_ftz(0.25f + ex2_ftz(fmaf(v, -1.4426950408889634f, -2.0f)));
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_of(float g) {
@@ -121,7 +139,7 @@ __device__ __forceinline__ float act_of(float g) {
 template <int ACT>
 __device__ __forceinline__ float2 act_grad(float g) {
   if (ACT == ACT_SILU) {
-    const float p = __fdividef(1.0f, 1.0f + __expf(-g));
+    const float p = g_sigmoid(1.0f, g);
     return make_float2(g * p, p * fmaf(g, 1.0f - p, 1.0f));
   }
   if (ACT == ACT_GELU) {
@@ -130,7 +148,7 @@ __device__ __forceinline__ float2 act_grad(float g) {
   }
   // past |g| = 30 p is 0 or 1 to the last bit: the clamp only keeps the cube finite (and keeps a NaN)
   const float c = fabsf(g) > 30.0f ? copysignf(30.0f, g) : g;
-  const float p = __fdividef(1.0f, 1.0f + __expf(-2.0f * kGeluC * fmaf(kGeluA * c * c, c, c)));
+  const float p = g_sigmoid(1.0f, 2.0f * kGeluC * fmaf(kGeluA * c * c, c, c));
   return make_float2(g * p, fmaf(2.0f * p * (1.0f - p), kGeluC * fmaf(3.0f * kGeluA * c * c, c, c), p));
 }
 

@@ -190,3 +190,30 @@ def test_norm_gradients_off_boundaries_repeat_their_bits(dtype, rows, cols, lead
     serial = 200 + (rows + 99) // 100
     assert L.worst(first[0], wx, wx.abs() * L.U[dtype] + mx * serial * 2.0 ** -24 + L.TINY[dtype]) <= 1
     assert L.worst(first[1], ww, ww.abs() * L.U[dtype] + mw * serial * 2.0 ** -24 + L.TINY[dtype]) <= 1
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("t", [3, 300])
+def test_the_activations_tails(act, t):
+    # gates down to where the activation leaves bf16's normal numbers, one a hidden unit, times an up of 2^100 that
+    # brings it back: x holds one feature for the gate and one for up
+    h = 256
+    # (act_of and its derivative are 1e-37 there; below it they go under the type's smallest normal)
+    last = {"silu": -88.5, "gelu": -12.5, "gelu_tanh": -9.8}[act]
+    g = torch.linspace(0.5 * last, last, h, device="cuda").to(BF16)
+    wg, wu = torch.zeros((h, 64), device="cuda", dtype=BF16), torch.zeros((h, 64), device="cuda", dtype=BF16)
+    wg[:, 0], wu[:, 1] = g, 2.0 ** 50
+    x = torch.zeros((t, 64), device="cuda", dtype=BF16)
+    x[:, 0], x[:, 1] = 1.0, 2.0 ** 50
+    out, gate, up = msb.gated_ffn(x, wg, wu, activation=act, save=True)
+    assert bool((gate == g).all()) and bool((up == 2.0 ** 100).all())
+    a, da = L.act(g.double(), act)
+    # The exponent's argument (at most 90, from up to six fp32 operations: 2^-21.5 relative) is off by 2^-15 and so is
+    # the exponential, relative to itself; gelu's erfc is closer.  Below 2^-126 fp32 steps by 2^-149.
+    bound = a.abs() * 2.0 ** 100 * (L.U[BF16] + 2.0 ** -14) + 2.0 ** (100 - 149) * g.double().abs()
+    assert L.worst(out, (a * 2.0 ** 100).expand_as(out), bound.expand_as(out)) <= 1
+    dh = torch.ones_like(out)
+    dx, dwg, dwu = msb.gated_ffn_backward(dh, x, wg, wu, gate, up, activation=act, grad_dtype=FP32)
+    # dWg[:, 0] = t dg: the derivative is p (1 + ...) with the same exponential, dg rounded once
+    bound = da.abs() * 2.0 ** 100 * (L.U[BF16] + 2.0 ** -13) + 2.0 ** (100 - 149) * 4 * g.double().abs() ** 2
+    assert L.worst(dwg[:, 0] / t, da * 2.0 ** 100, bound) <= 1
