@@ -550,6 +550,10 @@ msign_status gated_ffn(const void *x, const void *w_gate, const void *w_up, void
 /* gated_ffn_backward: from dh (tokens x h) and the kept gate and up,
  *   dg = dh up act'(gate),  du = dh act(gate)   (rounded to dtype)
  *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x.
+ * dg and du have dtype's range whatever grad_dtype is: in MSIGN_FP16 one past
+ * 65504 is infinite, one below 6e-5 has fewer digits and one below 3e-8 is
+ * zero, so that dh has to be scaled to stay between (as fp16 training scales
+ * its loss).
  * dx is dtype; dw_gate and dw_up (h x d, row stride dw_stride) are
  * grad_dtype: dtype or MSIGN_FP32.  dx may be NULL, and so may dw_gate and
  * dw_up together.  tokens = 0 writes zero weight gradients.  Outputs must

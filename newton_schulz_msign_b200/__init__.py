@@ -446,6 +446,9 @@ def mousse_direction(g, l_root, r_root, out=None, *, coeffs=None, eps=None, impr
 
 
 # ---------------------------------------------------------------- layer operators
+#
+# Like every call of this library they are not recorded by autograd: outputs
+# carry no graph, and gradients come of the *_backward calls.
 
 def _rows_layout(t, name, cols=None):
     """(rows, cols, stride) of a CUDA tensor whose last dim is dense and whose
@@ -535,7 +538,9 @@ def _on_stream(op):
             return op(*args, **kwargs)
     # (python -OO leaves no docstring to add to)
     if op.__doc__:
-        call.__doc__ = op.__doc__ + "\n\n    ``stream``: the stream to run on, for the outputs too (default: the current one)."
+        call.__doc__ = op.__doc__ + (
+            "\n\n    Autograd does not record the call: the outputs carry no graph."
+            "\n    ``stream``: the stream to run on, for the outputs too (default: the current one).")
     return call
 
 
@@ -765,7 +770,9 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, *, activation: str = "silu
     """Gradients of ``gated_ffn``: (dx, dw_gate, dw_up) from ``dh`` and the kept ``gate`` and ``up``.
 
     ``grad_dtype``: of the weight gradients, x's dtype (default) or float32;
-    either is what ``muon_step`` takes as grads (fp16 blocks: float32).
+    either is what ``muon_step`` takes as grads (fp16 blocks: float32).  The
+    gradients of gate and up are held in x's dtype on the way: in fp16 scale
+    ``dh`` so that dh * up and dh * act(gate) stay below 65504.
     ``need_dx`` / ``need_dw`` False leaves that part out (None in its place)."""
     torch = _torch()
     code, act = _dtype_code(x), _activation_code(activation)

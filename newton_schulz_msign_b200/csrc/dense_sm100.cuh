@@ -979,7 +979,11 @@ __device__ __forceinline__ void store_n(T* p, const float* v) {
 
 // dg = dh u act'(g) and du = dh act(g), one after the other in `out` with
 // rows of ldp elements (a multiple of 8).  HBM-bound; both are rounded to the
-// io type here, as the operands of the products that follow.
+// io type here, as the operands of the products that follow: a 16-bit MMA
+// takes no more, and splitting each into two operands would double the
+// products.  It costs dx and the weights' gradients a factor of sqrt 2 in error
+// (8192 x 4096 x 14336 bf16 2.3e-3 against 1.7e-3 for unrounded ones), and in
+// fp16 the range: past 65504 infinity, below 6e-5 fewer digits, below 3e-8 zero.
 //
 // 64 threads of a block take 512 columns, eight each, loaded by accesses of P
 // elements (what the rows' alignment allows: 8, 2 or 1); the block's four rows

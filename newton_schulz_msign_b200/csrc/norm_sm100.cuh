@@ -15,11 +15,12 @@
 //
 // Measured (B200, copy rate 6.54 TB/s): 8192 x 4096 bf16 with a residual 41.7
 // us (268 MB, 41.0 at the copy rate), to int8 39.8 (235 MB, 35.9; by now
-// bound by instructions), one row 2.3, gradients 56 (268 MB).
+// bound by instructions), one row 2.3, gradients 49 (268 MB).
 //
-// Rows whose addresses or width do not allow 16-byte accesses move element by
-// element; rows longer than 1024 threads hold take the *_loop kernels, which
-// read the row again for each pass (it is still in L1 or L2 then).
+// Rows off 16-byte boundaries move by 16 bytes about them where all matrices
+// of a call lie alike, else by elements; rows longer than 1024 threads hold
+// take the *_loop kernels, which read the row again for each pass (it is still
+// in L1 or L2 then).  norm_plan.h chooses.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -282,7 +283,8 @@ __device__ __forceinline__ void load_weight(const void* w, int w_f32, int c, flo
 // boundary, modulo the elements of 16 bytes), piece k of a row with phase ph
 // starts at column k vec - ph, and only its first and its last piece are not
 // whole (8192 rows with a residual, bf16: 1002 columns 17 us, by pairs 23;
-// 2001 33, one by one 61; 8191 137 and 224).
+// 2001 33, one by one 61; 8191 137 and 224).  The 16-bit form of four pieces a
+// thread still spills 8 to 16 bytes at its 64 registers.
 template <typename T>
 __device__ __forceinline__ int row_phase(const void* p, long long at) {
   return static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T) + static_cast<unsigned long long>(at)) %
@@ -726,7 +728,9 @@ __device__ __noinline__ float2 warp_sums(const T* z, const T* dy, const void* w,
 // NORM_FULL: every thread has a column and a row in every turn.  NORM_SHIFT:
 // rows off 16-byte boundaries, all matrices in the same phase (row_phase); a
 // thread's rows have one phase, so that its columns stay the same (16384 x 1001
-// bf16 with ds 44 us; by elements, dy and z read again for dw, 97).
+// bf16 with ds 44 us; by elements, dy and z read again for dw, 97).  Its 16-bit
+// form of two pieces a thread spills 48 bytes at 80 registers; the others, and
+// all of the two kinds above, none.
 //
 // What bounds it: 8192 x 4096 bf16 with ds 49 us, 41 of them HBM's; 3 are
 // dw_reduce_kernel, 1 the last turn of rows, the rest the first copies'
