@@ -457,9 +457,9 @@ msign_status mousse_direction(const void *G, void *out, msign_dtype io_dtype, in
  * counts).
  * Row counts and widths are at most 2^30, and a product has at most 2^29
  * tiles of 256 x 128 outputs (MSIGN_ERR_UNSUPPORTED beyond).
- * An output at the address of another buffer of its call is refused
- * (MSIGN_ERR_INVALID_ARG) where the entry point does not allow it; other
- * overlaps are not looked for.
+ * An output, or a workspace that the call needs, at the address of another
+ * buffer of the call is refused (MSIGN_ERR_INVALID_ARG) where the entry point
+ * does not allow it; other overlaps are not looked for.
  * Two calls that may run at the same time, two captured graphs among them,
  * need a workspace each.  Results do not depend on the order in which the
  * GPU runs a call's blocks: the same inputs give the same bits.

@@ -640,6 +640,7 @@ msign_status rms_norm_backward(const void* dy, const void* sum, const void* weig
   if (is_one_of(dx, {dy, sum, weight, dsum, dw}) || is_one_of(dw, {dy, sum, weight, dsum})) return MSIGN_ERR_INVALID_ARG;
   if (dw != nullptr && !workspace_ok(workspace, workspace_bytes, rms_norm_backward_workspace_size(rows, cols)))
     return MSIGN_ERR_WORKSPACE;
+  if (dw != nullptr && is_one_of(workspace, {dy, sum, weight, dsum, dx, dw})) return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   msign_status st = layer_state(&dev);
   if (st != MSIGN_OK) return st;
@@ -685,9 +686,10 @@ msign_status i8_matmul(const int8_t* a, const float* a_scale, const int8_t* b, c
   if (k == 0) return zero_rows(out, ldo, m, n, oes, stream);
   if (a == nullptr || b == nullptr || a_scale == nullptr || b_scale == nullptr) return MSIGN_ERR_INVALID_ARG;
   if (!on_elements({a_scale, b_scale}, 4) || !on_elements({out}, oes)) return MSIGN_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, workspace_bytes, i8_matmul_workspace_size(m, n, k, a, a_stride, b, b_stride)))
-    return MSIGN_ERR_WORKSPACE;
-  if (is_one_of(out, {a, b, a_scale, b_scale})) return MSIGN_ERR_INVALID_ARG;
+  const size_t need = i8_matmul_workspace_size(m, n, k, a, a_stride, b, b_stride);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return MSIGN_ERR_WORKSPACE;
+  if (is_one_of(out, {a, b, a_scale, b_scale}) || (need > 0 && is_one_of(workspace, {a, b, a_scale, b_scale, out})))
+    return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   msign_status st = layer_state(&dev);
   if (st != MSIGN_OK) return st;
@@ -768,9 +770,9 @@ msign_status gated_ffn(const void* x, const void* w_gate, const void* w_up, void
   if (is_one_of(out, {x, w_gate, w_up, gate_out, up_out}) || is_one_of(gate_out, {x, w_gate, w_up, up_out}) ||
       is_one_of(up_out, {x, w_gate, w_up}))
     return MSIGN_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, workspace_bytes,
-                    gated_ffn_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))
-    return MSIGN_ERR_WORKSPACE;
+  const size_t need = gated_ffn_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride);
+  if (!workspace_ok(workspace, workspace_bytes, need)) return MSIGN_ERR_WORKSPACE;
+  if (need > 0 && is_one_of(workspace, {x, w_gate, w_up, out, gate_out, up_out})) return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   if ((st = layer_state(&dev)) != MSIGN_OK) return st;
   Operand ox{x, tokens, d, stride_of(x_stride, d), 2}, og{w_gate, h, d, ldw, 2}, ou{w_up, h, d, ldw, 2};
@@ -857,6 +859,7 @@ msign_status gated_ffn_backward(const void* dh, const void* x, const void* w_gat
   if (!workspace_ok(workspace, workspace_bytes,
                     gated_ffn_backward_workspace_size(tokens, d, h, x, x_stride, w_gate, w_up, w_stride)))
     return MSIGN_ERR_WORKSPACE;
+  if (is_one_of(workspace, {dh, x, w_gate, w_up, gate, up, dx, dw_gate, dw_up})) return MSIGN_ERR_INVALID_ARG;
   DeviceState* dev = nullptr;
   if ((st = layer_state(&dev)) != MSIGN_OK) return st;
   Operand ox{x, tokens, d, ldx, 2}, og{w_gate, h, d, ldw, 2}, ou{w_up, h, d, ldw, 2};

@@ -218,6 +218,20 @@ def test_rms_norm_in_place_needs_the_inputs_row_stride(lib, outs, strides):
         assert in_place_status(lib, outs, strides, 4, q8=True) == BAD
 
 
+BIG = 1 << 24  # bytes enough for any of these workspaces
+
+
+@pytest.mark.parametrize("ws", range(6))
+def test_a_workspace_at_another_buffer_is_refused(lib, ws):
+    # (where the call needs one: rows of 65 elements have to be copied)
+    assert lib.rms_norm_backward(*(at(i) for i in range(6)), B, B, 4, 64, 0, 0, 0, 0, 1e-6, at(ws), BIG, None) == BAD
+    if ws < 5:
+        assert lib.i8_matmul(*(at(i) for i in range(5)), B, 4, 64, 65, 0, 0, 0, at(ws), BIG, None) == BAD
+    assert lib.gated_ffn(*(at(i) for i in range(6)), B, 0, 4, 65, 64, 0, 0, 0, 0, at(ws), BIG, None) == BAD
+    for i in (0, 3):  # any of the nine
+        assert lib.gated_ffn_backward(*(at(j) for j in range(9)), B, B, 0, 4, 64, 64, 0, 0, 0, 0, 0, 0, at(ws + i), BIG, None) == BAD
+
+
 # ---------------------------------------------------------------- addresses between elements
 
 def norm_at(lib, i, off, io=B, wd=F, q8=False):
